@@ -316,6 +316,158 @@ VDN_API vdn_status vdn_hybrid_attn_fwd_host(const void* q, const void* k, const 
                                             void* staging, size_t staging_bytes,
                                             const vdn_cfg* cfg, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Causal linear memory with a decay for each head.
+ *
+ * The hybrid call's linear branch sums phi(k) v^T over whole frame-chunks, in
+ * both directions, and needs the whole clip.  A model that produces frame after
+ * frame, or text token after token, reads the causal form of the same memory:
+ *
+ *   S_t = lambda_h S_{t-1} + k_t^T v_t     (d x d, fp32),   lambda_h = exp(log_decay[h])
+ *   out_t = scale * q_t S_t                (token t itself included)
+ *
+ * per batch entry and head, S before the first token = state_in (or 0).  Any
+ * feature map is the caller's, applied to q and k beforehand; the RMSNorm that
+ * follows is vdn_add_rmsnorm_fwd.  There is no counterpart on the article's
+ * pages: an interface addition, not part of the method.
+ *
+ *   vdn_linear_attn_fwd   whole sequences, state in and out;
+ *   vdn_linear_attn_bwd   the gradients by q, k, v and state_in;
+ *   vdn_linear_attn_step  one token of each of `batch` sequences, on a pool of
+ *                         states that is updated in place.
+ *
+ * log_decay is expected to be <= 0 (-infinity: lambda = 0, a token sees itself
+ * only); larger values follow the formula.  It is a constant of the model: no
+ * gradient by it is formed.
+ *
+ * Accumulation, states, scores and decay factors are fp32.
+ *
+ * Tensors are views: element (b, n, h, i) of a tensor lies at data + b *
+ * batch_stride + n * token_stride + h * head_stride + i, strides in elements
+ * (the head_dim elements of a row are contiguous), so that q, k and v may be
+ * slices of one projection.  data is 16-byte aligned and every stride a
+ * multiple of 16 bytes; an input's stride may be 0 (a broadcast), an output's
+ * only where that dimension has one entry.  Outputs must not overlap each other
+ * or an input.
+ *
+ * lengths (optional, device, one int32 per batch entry, clamped to [0, tokens]):
+ * batch entry b has lengths[b] tokens, and its later rows are padding.  Padding
+ * rows are not used whatever they hold, and the rows of out, dq, dk and dv
+ * there are written as zeros.  state_out is the state after the last real
+ * token: state_in (or 0) for a sequence without one.
+ *
+ * States are [batch][heads][head_dim (of k)][head_dim (of v)] fp32, 16-byte
+ * aligned, with the given distance between batch entries.  state_out may be
+ * state_in itself (same pointer and stride); any other overlap is not allowed.
+ * ---------------------------------------------------------------------- */
+
+typedef struct {
+  void* data;
+  int64_t batch_stride, token_stride, head_stride; /* elements */
+} vdn_view;
+
+typedef struct {
+  int32_t batch;          /* B >= 1 */
+  int32_t tokens;         /* N >= 0 (vdn_linear_attn_step: not read) */
+  int32_t heads;          /* 1 <= H <= 4096 */
+  int32_t head_dim;       /* d in {32, 64, 128} */
+  int32_t dtype;          /* vdn_dtype of q, k, v, out and their gradients */
+  float scale;            /* <= 0 selects 1/sqrt(head_dim) */
+  const float* log_decay; /* device [heads] fp32, 4-byte aligned */
+  const int32_t* lengths; /* device [batch] or NULL (all tokens); not read by the step */
+  const float* state_in;  /* fwd, bwd: S before the first token, or NULL (0) */
+  float* state_out;       /* fwd: S after the last token, or NULL; step: the pool of states */
+  const float* d_state_out; /* bwd: gradient by state_out, or NULL (0) */
+  float* d_state_in;      /* bwd: gradient by state_in, or NULL */
+  int64_t state_in_stride, state_out_stride;     /* elements between batch entries (step: between */
+  int64_t d_state_out_stride, d_state_in_stride; /* slots); 0 selects heads * head_dim^2 */
+  const int32_t* slots;   /* step: device [batch], the pool entry of each row, or NULL (row b: entry b) */
+  int32_t n_slots;        /* step: entries of the pool */
+  int32_t debug_flags;    /* VDN_POISON_WS, VDN_INJECT_TIMEOUT (tests); 0 in production */
+  void* workspace;        /* device, 256-byte aligned, >= vdn_linear_workspace_bytes; not used by the step */
+  size_t workspace_bytes;
+  int32_t* status_word;   /* optional device int32: VDN_ERR_TIMEOUT by a kernel that gave up,
+                             VDN_ERR_INVALID_ARG by the step for a slot >= n_slots */
+} vdn_linear_cfg;
+
+/* Host-only check of cfg's sizes, types and flags.  No CUDA call. */
+VDN_API vdn_status vdn_linear_validate(const vdn_linear_cfg* cfg);
+/* Bytes of workspace of the forward (backward = 0) or backward (1) call; 0 if
+ * cfg is invalid.  No CUDA call: the size holds for every device. */
+VDN_API size_t vdn_linear_workspace_bytes(const vdn_linear_cfg* cfg, int32_t backward);
+/* out and, where given, state_out, from q, k, v and state_in. */
+VDN_API vdn_status vdn_linear_attn_fwd(const vdn_view* q, const vdn_view* k, const vdn_view* v, const vdn_view* out,
+                                       const vdn_linear_cfg* cfg, void* stream);
+/* dq, dk, dv and, where given, d_state_in, from q, k, v, state_in, the
+ * gradient d_out by out and, where given, d_state_out. */
+VDN_API vdn_status vdn_linear_attn_bwd(const vdn_view* q, const vdn_view* k, const vdn_view* v, const vdn_view* d_out,
+                                       const vdn_view* dq, const vdn_view* dk, const vdn_view* dv,
+                                       const vdn_linear_cfg* cfg, void* stream);
+/* One token for each of cfg->batch rows (token_stride is not read): entry
+ * slots[b] of the pool cfg->state_out becomes lambda S + k_b^T v_b, and out_b =
+ * scale * q_b S of the new state.  A negative slot marks a padding row: no state
+ * is touched and its out row is written as zeros; so does a slot >= n_slots,
+ * which also writes VDN_ERR_INVALID_ARG to status_word.  Rows with the same slot
+ * are successive tokens of one sequence, taken in the order of the rows. */
+VDN_API vdn_status vdn_linear_attn_step(const vdn_view* q, const vdn_view* k, const vdn_view* v, const vdn_view* out,
+                                        const vdn_linear_cfg* cfg, void* stream);
+
+/* ------------------------------------------------------------------------
+ * RMSNorm with the residual's addition, and an output in 8 bits with scales.
+ *
+ *   h = x + residual,   y = h / sqrt(mean_i(h_i^2) + eps) * weight        (rows of `width` elements)
+ *
+ * in fp32; residual_out receives h rounded once to the tensors' type (the norm
+ * is taken of the unrounded sum).  The result is y in the tensors' type, or e4m3
+ * values with fp32 scales, y ~ value * scale, scale = max|y| / 448 over the row
+ * or over each 128 columns (the last group may be shorter), 1 where all are zero;
+ * values are rounded to nearest even.  A row that holds a NaN or an infinity
+ * gives what the formula gives: NaN values and, under a scale, a NaN scale
+ * where a NaN is in its reach.  Squares beyond fp32's range (elements above
+ * 1e17, or, with eps = 0, below 1e-17) are summed of the row multiplied by a
+ * power of two.
+ *
+ * Backward (of the tensor output; h is the stored residual_out, or x): with
+ * g = dy * weight, r = 1 / sqrt(mean(h^2) + eps):
+ *   dx = dh + r g - h r^3 mean(g h)    (the gradient by x and by residual; dh, the
+ *        gradient that reaches h from elsewhere, may be NULL)
+ *   dweight = sum over rows of dy h r   (fp32, summed in a fixed order)
+ *
+ * Row strides in elements, any value >= width; pointers aligned to their
+ * element.  Rows that are 16-byte aligned with a width divisible by 8 take
+ * vector loads.  x may be residual_out or, with VDN_NORM_TENSOR, out; outputs
+ * must not overlap otherwise.  There is no counterpart on the article's pages
+ * (its RMSNorm of the linear read is part of vdn_hybrid_attn_fwd).
+ * ---------------------------------------------------------------------- */
+
+/* Form of the norm's result. */
+typedef enum { VDN_NORM_TENSOR = 0, VDN_NORM_E4M3_ROW = 1, VDN_NORM_E4M3_GROUP = 2 } vdn_norm_output;
+
+typedef struct {
+  int64_t rows;        /* >= 0 */
+  int32_t width;       /* 1 <= width <= 2^20 */
+  int32_t dtype;       /* vdn_dtype of x, residual, residual_out, the tensor output, dy, dh, dx */
+  int32_t output;      /* vdn_norm_output; the backward takes VDN_NORM_TENSOR only */
+  float eps;           /* < 0 selects 1e-6 */
+  const float* weight; /* device [width] fp32, 4-byte aligned, or NULL (ones) */
+  int64_t x_stride, residual_stride, residual_out_stride, out_stride; /* elements; 0 selects width */
+  int64_t dy_stride, dh_stride, dx_stride; /* backward (h: x_stride) */
+  void* workspace;     /* backward with dweight: device, 256-byte aligned, >= vdn_norm_workspace_bytes */
+  size_t workspace_bytes;
+} vdn_norm_cfg;
+
+VDN_API vdn_status vdn_norm_validate(const vdn_norm_cfg* cfg);
+/* Bytes of workspace of vdn_add_rmsnorm_bwd with dweight; 0 if cfg is invalid. */
+VDN_API size_t vdn_norm_workspace_bytes(const vdn_norm_cfg* cfg);
+/* residual and residual_out may be NULL (h = x; h not stored).  scales: fp32
+ * [rows] (E4M3_ROW) or [rows, ceil(width / 128)] (E4M3_GROUP); not used by
+ * VDN_NORM_TENSOR. */
+VDN_API vdn_status vdn_add_rmsnorm_fwd(const void* x, const void* residual, void* residual_out, void* out,
+                                       float* scales, const vdn_norm_cfg* cfg, void* stream);
+/* dx and, where given, dweight [width] fp32. */
+VDN_API vdn_status vdn_add_rmsnorm_bwd(const void* h, const void* dy, const void* dh, void* dx, float* dweight,
+                                       const vdn_norm_cfg* cfg, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

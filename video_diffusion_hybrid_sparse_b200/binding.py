@@ -7,6 +7,7 @@ raises if the library has not been built: there is no other path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -28,7 +29,10 @@ EXPORTED = ["vdn_version", "vdn_status_string", "vdn_validate", "vdn_workspace_b
             "vdn_state_scan", "vdn_sparse_softmax", "vdn_softmax_and_scan", "vdn_readout_merge",
             "vdn_sparse_softmax_merge",
             "vdn_hybrid_attn_fwd_static",
-            "vdn_static_scratch_bytes", "vdn_host_staging_bytes", "vdn_hybrid_attn_fwd_host", "vdn_export_states"]
+            "vdn_static_scratch_bytes", "vdn_host_staging_bytes", "vdn_hybrid_attn_fwd_host", "vdn_export_states",
+            "vdn_linear_validate", "vdn_linear_workspace_bytes", "vdn_linear_attn_fwd", "vdn_linear_attn_bwd",
+            "vdn_linear_attn_step", "vdn_norm_validate", "vdn_norm_workspace_bytes", "vdn_add_rmsnorm_fwd",
+            "vdn_add_rmsnorm_bwd"]
 
 
 class VdnError(RuntimeError):
@@ -50,6 +54,35 @@ class VdnCfg(ctypes.Structure):
         ("export_fwd", ctypes.c_void_p), ("export_bwd", ctypes.c_void_p),
         ("output_mode", ctypes.c_int32), ("softmax_precision", ctypes.c_int32),
         ("out_linear", ctypes.c_void_p), ("readout_mode", ctypes.c_int32),
+    ]
+
+
+class VdnView(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class VdnLinearCfg(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int32), ("tokens", ctypes.c_int32), ("heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32), ("scale", ctypes.c_float),
+        ("log_decay", ctypes.c_void_p), ("lengths", ctypes.c_void_p),
+        ("state_in", ctypes.c_void_p), ("state_out", ctypes.c_void_p),
+        ("d_state_out", ctypes.c_void_p), ("d_state_in", ctypes.c_void_p),
+        ("state_in_stride", ctypes.c_int64), ("state_out_stride", ctypes.c_int64),
+        ("d_state_out_stride", ctypes.c_int64), ("d_state_in_stride", ctypes.c_int64),
+        ("slots", ctypes.c_void_p), ("n_slots", ctypes.c_int32), ("debug_flags", ctypes.c_int32),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t), ("status_word", ctypes.c_void_p),
+    ]
+
+
+class VdnNormCfg(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("width", ctypes.c_int32), ("dtype", ctypes.c_int32), ("output", ctypes.c_int32),
+        ("eps", ctypes.c_float), ("weight", ctypes.c_void_p),
+        ("x_stride", ctypes.c_int64), ("residual_stride", ctypes.c_int64), ("residual_out_stride", ctypes.c_int64),
+        ("out_stride", ctypes.c_int64), ("dy_stride", ctypes.c_int64), ("dh_stride", ctypes.c_int64),
+        ("dx_stride", ctypes.c_int64), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
     ]
 
 
@@ -85,9 +118,21 @@ def library() -> ctypes.CDLL:
         lib.vdn_host_staging_bytes.restype = ctypes.c_size_t
         lib.vdn_host_staging_bytes.argtypes = [C]
         lib.vdn_hybrid_attn_fwd_host.argtypes = [P, P, P, P, P, P, P, P, P, ctypes.c_size_t, C, P]
+        V, L, R = ctypes.POINTER(VdnView), ctypes.POINTER(VdnLinearCfg), ctypes.POINTER(VdnNormCfg)
+        lib.vdn_linear_validate.argtypes = [L]
+        lib.vdn_linear_workspace_bytes.restype = ctypes.c_size_t
+        lib.vdn_linear_workspace_bytes.argtypes = [L, ctypes.c_int32]
+        lib.vdn_linear_attn_fwd.argtypes = [V, V, V, V, L, P]
+        lib.vdn_linear_attn_bwd.argtypes = [V, V, V, V, V, V, V, L, P]
+        lib.vdn_linear_attn_step.argtypes = [V, V, V, V, L, P]
+        lib.vdn_norm_validate.argtypes = [R]
+        lib.vdn_norm_workspace_bytes.restype = ctypes.c_size_t
+        lib.vdn_norm_workspace_bytes.argtypes = [R]
+        lib.vdn_add_rmsnorm_fwd.argtypes = [P, P, P, P, P, R, P]
+        lib.vdn_add_rmsnorm_bwd.argtypes = [P, P, P, P, P, R, P]
         for name in EXPORTED:
             if name not in ("vdn_version", "vdn_status_string", "vdn_workspace_bytes", "vdn_static_scratch_bytes",
-                            "vdn_host_staging_bytes"):
+                            "vdn_host_staging_bytes", "vdn_linear_workspace_bytes", "vdn_norm_workspace_bytes"):
                 getattr(lib, name).restype = ctypes.c_int
         _lib = lib
     return _lib
@@ -411,3 +456,276 @@ def membership_device(F: int, C: int, P: int = 1, T: int = 0, device="cuda",
 def validate(s: Shape, **kw) -> int:
     """Status code of the host-side argument check (no CUDA call)."""
     return library().vdn_validate(ctypes.byref(make_cfg(s, **kw)))
+
+
+# ---------------------------------------------------------------- causal linear memory and residual RMSNorm
+
+NORM_OUT_TENSOR, NORM_OUT_E4M3_ROW, NORM_OUT_E4M3_GROUP = 0, 1, 2
+_DTYPES = {torch.bfloat16: VDN_BF16, torch.float32: VDN_FP32}
+_HERE = contextlib.nullcontext()
+
+
+def _on(t: torch.Tensor, stream):
+    """Context in which a call on ``t`` allocates and launches: its device, and
+    ``stream`` (of that device) when one is given."""
+    if not t.is_cuda:
+        raise ValueError("expected CUDA tensors")
+    if stream is not None:
+        if stream.device != t.device:
+            raise ValueError("the stream and the tensors are on different devices")
+        return torch.cuda.stream(stream)
+    return _HERE if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+
+
+def _match(name, t, shape, dtype, device):
+    """``t`` has this shape, type and device and elements of its last dimension side by side."""
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name}: expected {tuple(shape)} {dtype} on {device}, got {tuple(t.shape)} {t.dtype} "
+                         f"on {t.device}")
+    if len(shape) > 1 and t.stride(-1) != 1 and shape[-1] != 1:
+        raise ValueError(f"{name}: the elements of the last dimension must be contiguous")
+
+
+def _view(t: torch.Tensor) -> VdnView:
+    """[B, N, H, d] or (a step's) [B, H, d]."""
+    s = t.stride()
+    return VdnView(t.data_ptr(), s[0], s[1], s[2]) if len(s) == 4 else VdnView(t.data_ptr(), s[0], 0, s[1])
+
+
+def _state(name, t, B, H, d, device):
+    """Pointer and batch stride of [B, H, d, d] fp32 states (the last three dimensions contiguous)."""
+    if t is None:
+        return None, 0
+    if tuple(t.shape) != (B, H, d, d) or t.dtype != torch.float32 or t.device != device:
+        raise ValueError(f"{name}: expected {(B, H, d, d)} torch.float32 on {device}, got {tuple(t.shape)} {t.dtype} "
+                         f"on {t.device}")
+    if t.stride()[1:] != (d * d, d, 1):
+        raise ValueError(f"{name}: the last three dimensions must be contiguous")
+    return t.data_ptr(), t.stride(0) if B > 1 else H * d * d
+
+
+def _flat(name, t, n, dtype, device):
+    """Pointer of a contiguous vector of n elements, or None."""
+    if t is None:
+        return None
+    if tuple(t.shape) != (n,) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous ({n},) {dtype} on {device}, got {tuple(t.shape)} {t.dtype} "
+                         f"on {t.device}")
+    return t.data_ptr()
+
+
+def _linear_cfg(q, log_decay, scale, lengths, status, debug_flags) -> VdnLinearCfg:
+    if q.dim() != 4 or q.dtype not in _DTYPES:
+        raise ValueError(f"q: expected a [B, N, H, d] bf16 or fp32 tensor, got {tuple(q.shape)} {q.dtype}")
+    B, N, H, d = q.shape
+    cfg = VdnLinearCfg()
+    cfg.batch, cfg.tokens, cfg.heads, cfg.head_dim, cfg.dtype = B, N, H, d, _DTYPES[q.dtype]
+    cfg.scale = scale
+    cfg.log_decay = _flat("log_decay", log_decay, H, torch.float32, q.device)
+    cfg.lengths = _flat("lengths", lengths, B, torch.int32, q.device)
+    cfg.status_word = _ptr(status)
+    cfg.debug_flags = debug_flags
+    return cfg
+
+
+def _linear_workspace(cfg, backward, workspace, device):
+    """``workspace``, or a new one from the caching allocator: it belongs to the
+    current stream (and, during a capture, to that graph), so calls on several
+    streams and captured graphs share none."""
+    if workspace is None:
+        n = library().vdn_linear_workspace_bytes(ctypes.byref(cfg), backward)
+        if n == 0:
+            _check(library().vdn_linear_validate(ctypes.byref(cfg)), "vdn_linear_workspace_bytes")
+        workspace = torch.empty(n, dtype=torch.uint8, device=device)
+    cfg.workspace, cfg.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return workspace
+
+
+def linear_workspace_bytes(B: int, N: int, H: int, d: int, dtype=torch.bfloat16, backward: bool = False) -> int:
+    """Bytes of workspace of :func:`linear_attn_fwd` (``backward``: :func:`linear_attn_bwd`)."""
+    cfg = VdnLinearCfg()
+    cfg.batch, cfg.tokens, cfg.heads, cfg.head_dim, cfg.dtype = B, N, H, d, _DTYPES[dtype]
+    n = library().vdn_linear_workspace_bytes(ctypes.byref(cfg), int(backward))
+    if n == 0:
+        _check(library().vdn_linear_validate(ctypes.byref(cfg)), "vdn_linear_workspace_bytes")
+    return n
+
+
+def linear_attn_fwd(q, k, v, log_decay, *, scale: float = 0.0, state_in=None, state_out=None, lengths=None, out=None,
+                    workspace=None, status=None, stream=None, debug_flags: int = 0) -> torch.Tensor:
+    """The causal linear memory with a decay for each head, over whole sequences.
+
+    out_t = scale * q_t S_t with S_t = exp(log_decay[h]) S_{t-1} + k_t^T v_t.
+
+    q, k, v (and out): [B, N, H, d] of one dtype (bf16 or fp32), d in {32, 64,
+    128}, any strides that are multiples of 16 bytes with contiguous rows (slices
+    of one projection serve); log_decay: [H] fp32, a constant (no gradient);
+    state_in, state_out: [B, H, d, d] fp32 or None, state_out is written and may
+    be state_in; lengths: [B] int32 or None, the tokens of each padded sequence:
+    rows behind them come out as zeros.  ``scale`` <= 0 selects d**-0.5."""
+    with _on(q, stream):
+        cfg = _linear_cfg(q, log_decay, scale, lengths, status, debug_flags)
+        B, N, H, d = q.shape
+        _match("q", q, q.shape, q.dtype, q.device)
+        _match("k", k, q.shape, q.dtype, q.device)
+        _match("v", v, q.shape, q.dtype, q.device)
+        if out is None:
+            out = torch.empty((B, N, H, d), dtype=q.dtype, device=q.device)
+        else:
+            _match("out", out, q.shape, q.dtype, q.device)
+        cfg.state_in, cfg.state_in_stride = _state("state_in", state_in, B, H, d, q.device)
+        cfg.state_out, cfg.state_out_stride = _state("state_out", state_out, B, H, d, q.device)
+        workspace = _linear_workspace(cfg, 0, workspace, q.device)
+        code = library().vdn_linear_attn_fwd(_view(q), _view(k), _view(v), _view(out), ctypes.byref(cfg), _stream())
+        _check(code, "vdn_linear_attn_fwd")
+    return out
+
+
+def linear_attn_bwd(q, k, v, log_decay, d_out, *, scale: float = 0.0, state_in=None, d_state_out=None,
+                    d_state_in=None, lengths=None, dq=None, dk=None, dv=None, workspace=None, status=None, stream=None,
+                    debug_flags: int = 0):
+    """Gradients (dq, dk, dv) of :func:`linear_attn_fwd` by q, k and v, from the
+    gradient ``d_out`` by its output and, where given, ``d_state_out`` by its last
+    state ([B, H, d, d] fp32); ``d_state_in``, where given, receives the gradient
+    by state_in.  Nothing of the forward call is kept: q, k, v and state_in are
+    read again.  Rows behind ``lengths`` get zeros."""
+    with _on(q, stream):
+        cfg = _linear_cfg(q, log_decay, scale, lengths, status, debug_flags)
+        B, N, H, d = q.shape
+        for name, t in (("q", q), ("k", k), ("v", v), ("d_out", d_out)):
+            _match(name, t, q.shape, q.dtype, q.device)
+        grads = []
+        for name, t in (("dq", dq), ("dk", dk), ("dv", dv)):
+            if t is None:
+                t = torch.empty((B, N, H, d), dtype=q.dtype, device=q.device)
+            else:
+                _match(name, t, q.shape, q.dtype, q.device)
+            grads.append(t)
+        cfg.state_in, cfg.state_in_stride = _state("state_in", state_in, B, H, d, q.device)
+        cfg.d_state_out, cfg.d_state_out_stride = _state("d_state_out", d_state_out, B, H, d, q.device)
+        cfg.d_state_in, cfg.d_state_in_stride = _state("d_state_in", d_state_in, B, H, d, q.device)
+        workspace = _linear_workspace(cfg, 1, workspace, q.device)
+        code = library().vdn_linear_attn_bwd(_view(q), _view(k), _view(v), _view(d_out), *map(_view, grads),
+                                             ctypes.byref(cfg), _stream())
+        _check(code, "vdn_linear_attn_bwd")
+    return tuple(grads)
+
+
+def linear_attn_step(q, k, v, log_decay, state, *, slots=None, scale: float = 0.0, out=None, status=None,
+                     stream=None) -> torch.Tensor:
+    """One token for each of B sequences: the recurrent form of :func:`linear_attn_fwd`.
+
+    q, k, v (and out): [B, H, d]; state: the pool [n, H, d, d] fp32, updated in
+    place; slots: [B] int32, the pool entry of each row (None: row b has entry
+    b).  A negative slot marks a padding row (out is zero there, no state is
+    touched), and so does one past the pool, which also sets ``status`` (int32) to
+    1.  Rows of the same slot are successive tokens, in the order of the rows."""
+    with _on(q, stream):
+        if q.dim() != 3 or q.dtype not in _DTYPES:
+            raise ValueError(f"q: expected a [B, H, d] bf16 or fp32 tensor, got {tuple(q.shape)} {q.dtype}")
+        B, H, d = q.shape
+        for name, t in (("q", q), ("k", k), ("v", v)):
+            _match(name, t, q.shape, q.dtype, q.device)
+        if out is None:
+            out = torch.empty((B, H, d), dtype=q.dtype, device=q.device)
+        else:
+            _match("out", out, q.shape, q.dtype, q.device)
+        cfg = VdnLinearCfg()
+        cfg.batch, cfg.heads, cfg.head_dim, cfg.dtype, cfg.scale = B, H, d, _DTYPES[q.dtype], scale
+        cfg.log_decay = _flat("log_decay", log_decay, H, torch.float32, q.device)
+        cfg.state_out, cfg.state_out_stride = _state("state", state, state.shape[0], H, d, q.device)
+        cfg.slots, cfg.n_slots = _flat("slots", slots, B, torch.int32, q.device), state.shape[0]
+        cfg.status_word = _ptr(status)
+        code = library().vdn_linear_attn_step(_view(q), _view(k), _view(v), _view(out), ctypes.byref(cfg), _stream())
+        _check(code, "vdn_linear_attn_step")
+    return out
+
+
+def _rows(name, t, shape, dtype, device):
+    """Pointer and row stride of a [rows, W] tensor."""
+    if t is None:
+        return None, 0
+    _match(name, t, shape, dtype, device)
+    if shape[0] <= 1:
+        return t.data_ptr(), shape[1]
+    if t.stride(0) < shape[1]:
+        raise ValueError(f"{name}: rows must not overlap")
+    return t.data_ptr(), t.stride(0)
+
+
+def _norm_cfg(x, weight, eps) -> VdnNormCfg:
+    if x.dim() != 2 or x.dtype not in _DTYPES:
+        raise ValueError(f"expected a [rows, width] bf16 or fp32 tensor, got {tuple(x.shape)} {x.dtype}")
+    cfg = VdnNormCfg()
+    cfg.rows, cfg.width, cfg.dtype, cfg.eps = x.shape[0], x.shape[1], _DTYPES[x.dtype], eps
+    cfg.weight = _flat("weight", weight, x.shape[1], torch.float32, x.device)
+    return cfg
+
+
+def add_rmsnorm_fwd(x, weight=None, *, residual=None, residual_out=None, eps: float = -1.0,
+                    out_mode: int = NORM_OUT_TENSOR, out=None, scales=None, stream=None):
+    """RMSNorm of h = x + residual: y = h / sqrt(mean(h**2) + eps) * weight.
+
+    x, residual, residual_out: [rows, W], bf16 or fp32, any row stride;
+    residual_out, where given, receives h in the tensors' type (it may be x or
+    residual); weight: [W] fp32 or None (ones).  Returns y in the tensors' type,
+    or, for NORM_OUT_E4M3_ROW / NORM_OUT_E4M3_GROUP, (values, scales): e4m3
+    [rows, W] and fp32 scales [rows, 1] / [rows, ceil(W / 128)], y ~ value *
+    scale."""
+    with _on(x, stream):
+        cfg = _norm_cfg(x, weight, eps)
+        rows, W = x.shape
+        cfg.output = out_mode
+        if out_mode not in (NORM_OUT_TENSOR, NORM_OUT_E4M3_ROW, NORM_OUT_E4M3_GROUP):
+            raise VdnError(1, "vdn_add_rmsnorm_fwd")
+        quant = out_mode != NORM_OUT_TENSOR
+        kind = torch.float8_e4m3fn if quant else x.dtype
+        if out is None:
+            out = torch.empty((rows, W), dtype=kind, device=x.device)
+        groups = (1 if out_mode == NORM_OUT_E4M3_ROW else (W + 127) // 128) if quant else 0
+        if quant and scales is None:
+            scales = torch.empty((rows, groups), dtype=torch.float32, device=x.device)
+        px, cfg.x_stride = _rows("x", x, (rows, W), x.dtype, x.device)
+        pr, cfg.residual_stride = _rows("residual", residual, (rows, W), x.dtype, x.device)
+        ps, cfg.residual_out_stride = _rows("residual_out", residual_out, (rows, W), x.dtype, x.device)
+        po, cfg.out_stride = _rows("out", out, (rows, W), kind, x.device)
+        if quant:
+            _match("scales", scales, (rows, groups), torch.float32, x.device)
+            if not scales.is_contiguous():
+                raise ValueError("scales: must be contiguous")
+        code = library().vdn_add_rmsnorm_fwd(px, pr, ps, po, _ptr(scales) if quant else None, ctypes.byref(cfg),
+                                             _stream())
+        _check(code, "vdn_add_rmsnorm_fwd")
+    return (out, scales) if quant else out
+
+
+def add_rmsnorm_bwd(h, weight, dy, *, dh=None, eps: float = -1.0, dx=None, dweight=None, want_dweight: bool = True,
+                    workspace=None, stream=None):
+    """Gradients (dx, dweight) of :func:`add_rmsnorm_fwd` with the tensor output:
+    dx, by x and equally by residual, in the tensors' type, and dweight [W] fp32
+    (None unless ``want_dweight``).  h: the stored residual_out (or x); dh: the
+    gradient that reaches h from elsewhere, or None."""
+    with _on(h, stream):
+        cfg = _norm_cfg(h, weight, eps)
+        rows, W = h.shape
+        if dx is None:
+            dx = torch.empty((rows, W), dtype=h.dtype, device=h.device)
+        if not want_dweight:
+            dweight = None
+        elif dweight is None:
+            dweight = torch.empty(W, dtype=torch.float32, device=h.device)
+        ph, cfg.x_stride = _rows("h", h, (rows, W), h.dtype, h.device)
+        pdy, cfg.dy_stride = _rows("dy", dy, (rows, W), h.dtype, h.device)
+        pdh, cfg.dh_stride = _rows("dh", dh, (rows, W), h.dtype, h.device)
+        pdx, cfg.dx_stride = _rows("dx", dx, (rows, W), h.dtype, h.device)
+        pdw = _flat("dweight", dweight, W, torch.float32, h.device)
+        if pdw is not None:
+            if workspace is None:
+                n = library().vdn_norm_workspace_bytes(ctypes.byref(cfg))
+                if n == 0:
+                    _check(library().vdn_norm_validate(ctypes.byref(cfg)), "vdn_norm_workspace_bytes")
+                workspace = torch.empty(n, dtype=torch.uint8, device=h.device)
+            cfg.workspace, cfg.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        code = library().vdn_add_rmsnorm_bwd(ph, pdy, pdh, pdx, pdw, ctypes.byref(cfg), _stream())
+        _check(code, "vdn_add_rmsnorm_bwd")
+    return dx, dweight

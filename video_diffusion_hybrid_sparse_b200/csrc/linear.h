@@ -1,0 +1,135 @@
+// linear.h - plan, parameter blocks and host launchers of the causal linear
+// memory with a decay for each head (vdn_linear_attn_fwd / _bwd / _step).
+//
+// All four results of the forward and backward calls are one operation, a
+// "job", with the tensors in other roles.  With rows taken in walk order (token
+// order, or its reverse):
+//
+//   o_i = alpha sum_{j <= i} lambda^(i-j) (x_i . y_j) z_j + factor_i x_i W,
+//
+//   result   walk      x      y      z      state W before the walk
+//   out      forward   q      k      v      state_in
+//   dq       forward   d_out  v      k      state_in, transposed
+//   dk       reverse   v      d_out  q      d_state_out / alpha, transposed
+//   dv       reverse   k      q      d_out  d_state_out / alpha
+//
+// (alpha = scale).  Split at chunk ends: with n rows in the chunk, p = 0..n-1
+// the row's place in walk order and W the state before it,
+//
+//   factor of row p on W:  alpha lambda^(p + e),       e = 1 forward, 0 reverse
+//   W after the chunk:     lambda^n W + sum_p lambda^(n - p - e) y_p^T z_p
+//
+// which needs no division by lambda: the reverse walk carries lambda R instead
+// of R, so that the gradient by state_in is alpha times the last W.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "plan.h"
+
+namespace vdn {
+
+constexpr int kLinSms = 148;          // CTAs a wave holds (one for each SM of a B200)
+constexpr int kLinMaxGrid = 2 * kLinSms;  // most ranges a walk is cut into
+constexpr int kLinSimtChunk = 32;     // rows of a chunk: fp32 kernels and head_dim 32
+constexpr int kLinTcChunk = 128;      // rows of a chunk: tensor-core kernels
+
+struct LinView {
+  void* p;
+  long long sb, sn, sh;  // elements
+};
+
+// The chunks of every (batch, head), (batch, head)-major and in walk order,
+// form one list; CTA j takes [start(j), start(j + 1)).  Where a range begins
+// inside a head, the state before it is the sum of what the earlier ranges of
+// that head leave: each range's own share ("part") is formed by a first kernel,
+// a scan over the ranges adds them up, and the walk starts from the result.
+struct LinPlan {
+  int chunk;        // rows of a chunk
+  int nc;           // chunks of a head
+  int grid;         // ranges
+  int split;        // a range may begin inside a head
+  long long total;  // chunks of all heads
+
+  VDN_HD long long start(int j) const { return total * j / grid; }
+  // the range that holds chunk t of the list
+  VDN_HD int range_of(long long t) const { return (int)(((t + 1) * grid + total - 1) / total - 1); }
+};
+
+// Real rows of the chunks [u0, u1) (walk order) of a head with n tokens.
+VDN_HD int lin_rows(int u0, int u1, int n, const LinPlan& pl, int reverse) {
+  const int lo = reverse ? pl.nc - u1 : u0, hi = reverse ? pl.nc - u0 : u1;
+  const long long most = (long long)(hi - lo) * pl.chunk, have = (long long)n - (long long)lo * pl.chunk;
+  return (int)(have < 0 ? 0 : have < most ? have : most);
+}
+
+struct LinJob {
+  LinView x, y, z, o;
+  int reverse;
+  int transposed;        // the states in memory are [z][y] for this job
+  const float* init;     // state before the walk or null; entries init_stride apart, [H, D, D] each
+  long long init_stride;
+  float init_mul;
+  const float* s_in;     // [grid, D, D]: state before range j (natural orientation of its walk)
+  const float* s_head;   // [grid, D, D] or null: copies of `init` for the head that range j begins and does not
+                         // end (its last range may overwrite `init`: state_out may be state_in)
+  float* final_out;      // state after the walk, or null
+  long long final_stride;
+  float final_mul;
+};
+
+struct LinOutParams {
+  LinPlan pl;
+  int B, N, H, n_jobs;
+  float alpha;
+  const float* log_decay;
+  const int* lengths;
+  int* status;
+  int* record;
+  int inject_timeout;
+  LinJob job[3];
+};
+
+// One walk's states: parts of the ranges, then their scan.
+struct LinWalk {
+  LinView y, z;
+  int reverse;
+  float* parts;        // [grid, D, D]
+  float* s_in;         // [grid, D, D]
+  float* s_head;       // [grid, D, D] or null (LinJob::s_head)
+  const float* init;
+  long long init_stride;
+  float init_mul;
+};
+
+struct LinStateParams {
+  LinPlan pl;
+  int B, N, H, n_walks;
+  const float* log_decay;
+  const int* lengths;
+  int* status;
+  int* record;
+  LinWalk walk[2];
+};
+
+struct LinStepParams {
+  LinView q, k, v, o;
+  int B, H;
+  float scale;
+  const float* log_decay;
+  float* pool;
+  long long slot_stride;
+  const int* slots;
+  int n_slots;
+  int* status;
+};
+
+// fp32: 1 for fp32 tensors, 0 for bf16
+cudaError_t launch_lin_states_simt(const LinStateParams& p, int D, int fp32, cudaStream_t st);
+cudaError_t launch_lin_scan(const LinStateParams& p, int D, cudaStream_t st);
+cudaError_t launch_lin_out_simt(const LinOutParams& p, int D, int fp32, cudaStream_t st);
+cudaError_t launch_lin_step(const LinStepParams& p, int D, int fp32, cudaStream_t st);
+
+}  // namespace vdn
