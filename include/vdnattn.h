@@ -340,7 +340,14 @@ VDN_API vdn_status vdn_hybrid_attn_fwd_host(const void* q, const void* k, const 
  * only); larger values follow the formula.  It is a constant of the model: no
  * gradient by it is formed.
  *
- * Accumulation, states, scores and decay factors are fp32.
+ * Accumulation, states and decay factors are fp32.  fp32 tensors are computed
+ * in fp32 throughout.  The contractions of bf16 tensors run on the tensor
+ * cores: decayed scores and the state are rounded to bf16 as operands of the
+ * read (not in the carried state), and decayed keys enter the state in two or
+ * three bf16 parts (2^-16 of a term, 2^-24 of one whose decay to the end is
+ * above 2^-4).  A token's contribution may end where its decay has fallen below
+ * 2^-150.  A NaN or an infinity in a real token's row may reach earlier rows of
+ * its 128-row chunk too.
  *
  * Tensors are views: element (b, n, h, i) of a tensor lies at data + b *
  * batch_stride + n * token_stride + h * head_stride + i, strides in elements

@@ -58,8 +58,8 @@ def check(got, ref, what, dtype, d, n):
     fp32 results (fp32 tensors, all states): a value is a chain of at most d + n +
     64 roundings of 2^-24 (dot products, sums over tokens, the decay's own
     error), each relative to a partial sum that mag bounds.  States of bf16
-    tensors: a decayed key is kept in two bf16 parts, the second one's rounding
-    is 2^-8 of 2^-8 of the key.
+    tensors: a decayed key is kept in three bf16 parts (2^-24 of it), or in two
+    (2^-16) where its weight in the state is below 2^-4 of the largest.
     bf16 results: a term's decayed score, or the state it is read from, is
     rounded to bf16 once (2^-8 of mag), the result once (2^-8 of itself)."""
     a, (r, mag) = got.double(), ref

@@ -64,6 +64,66 @@ def test_backward(B, N, H, d, dtype):
             R.check(got, ref[name], name, dtype, d, N)
 
 
+@pytest.mark.parametrize("B,N,H,d", [(1, 4000, 2, 128), (2, 3001, 1, 64), (1, 2500, 3, 32), (150, 400, 1, 64), (1, 1300, 160, 32)])
+def test_ranges(B, N, H, d):
+    """Heads cut into ranges whose states are formed first: few long heads, more heads than a wave holds; state handed in
+    and out in place; the state in fp32 as near as fp32 sums are, in norm."""
+    q, k, v, do = tensors(B, N, H, d, BF16, names="qkvo")
+    ld, s0, ds = decays(H)[torch.arange(H) * 5 % min(H, 6)], states(B, H, d, 5), states(B, H, d, 6)
+    ref = R.forward(q, k, v, ld, d ** -0.5, s0)
+    state = s0.clone()
+    out = vb.linear_attn_fwd(q, k, v, ld, state_in=state, state_out=state, debug_flags=vb.POISON_WS)
+    R.check(out, ref["out"], "out", BF16, d, N)
+    R.check(state, ref["state"], "state", BF16, d, N)
+    assert (state.double() - ref["state"][0]).norm() <= 1e-6 * ref["state"][0].norm()
+    ref = R.backward(q, k, v, ld, d ** -0.5, do, s0, ds)
+    din = torch.empty_like(s0)
+    grads = vb.linear_attn_bwd(q, k, v, ld, do, state_in=s0, d_state_out=ds, d_state_in=din, debug_flags=vb.POISON_WS)
+    for name, got in zip(("dq", "dk", "dv", "d_state_in"), (*grads, din)):
+        R.check(got, ref[name], name, BF16, d, N)
+
+
+def test_decay_beyond_the_ranges():
+    """Decays that end inside a chunk, a range or never, in one long head each; keys only in the far past."""
+    N, H, d = 9000, 6, 64
+    q, k, v = tensors(1, N, H, d, BF16)
+    ld = torch.tensor([0.0, -1e-4, -0.004, -0.03, -0.5, -3.0], device="cuda")
+    for lo in (0, N - 300):
+        k2 = k.clone()
+        k2[:, :lo] = 0
+        if lo:
+            k2[:, lo + 40:] = 0
+        ref = R.forward(q, k2, v, ld, 0.2)
+        state = torch.empty(1, H, d, d, device="cuda")
+        out = vb.linear_attn_fwd(q, k2, v, ld, scale=0.2, state_out=state)
+        R.check(out, ref["out"], "out", BF16, d, N)
+        R.check(state, ref["state"], "state", BF16, d, N)
+
+
+def test_one_row_for_all_tokens():
+    """A tensor whose token stride is 0 has no TMA view: the other kernels serve it."""
+    B, N, H, d = 2, 300, 2, 64
+    q, _, v = tensors(B, N, H, d, BF16)
+    k = tensors(B, 1, H, d, BF16)[0].expand(B, N, H, d)
+    ld = decays(H)
+    ref = R.forward(q, k, v, ld, d ** -0.5)
+    R.check(vb.linear_attn_fwd(q, k, v, ld), ref["out"], "out", BF16, d, N)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_injected_timeout(d):
+    """A wait that runs out ends the call with VDN_ERR_TIMEOUT in the status word; the context stays usable."""
+    q, k, v = tensors(1, 500, 2, d, BF16)
+    ld = decays(2)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    vb.linear_attn_fwd(q, k, v, ld, status=status, debug_flags=vb.INJECT_TIMEOUT)
+    assert int(status) == 6
+    status.zero_()
+    ref = R.forward(q, k, v, ld, d ** -0.5)
+    R.check(vb.linear_attn_fwd(q, k, v, ld, status=status), ref["out"], "out", BF16, d, 500)
+    assert int(status) == 0
+
+
 @pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
 @pytest.mark.parametrize("N,d", [(70, 32), (300, 64), (600, 128)])
 def test_padded_batch(N, d, dtype):

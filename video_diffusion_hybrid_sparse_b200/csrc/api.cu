@@ -11,6 +11,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "kernels.h"
+#include "tma_encode.h"
 #include "vdnattn.h"
 
 namespace vdn {
@@ -169,23 +170,6 @@ int* record_ptr(const vdn_cfg* cfg, const Geom& g) {
 }
 
 // ---------------------------------------------------------------- TMA descriptors
-
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  });
-  return fn;
-}
 
 // 2-D bf16 view [rows, H*Dp] (row pitch H*Dp*2 bytes), box box_rows rows x
 // 64 columns, 128-byte swizzle, zero fill out of bounds.

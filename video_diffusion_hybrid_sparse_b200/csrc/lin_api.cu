@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 
 #include <nvtx3/nvToolsExt.h>
 
@@ -75,19 +76,28 @@ LinView view(const vdn_view* v) {
 
 // ---------------------------------------------------------------- plan and workspace
 
-bool on_tensor_cores(const vdn_linear_cfg*) { return false; }
+// bf16 goes to the tensor cores.  A tensor whose tokens are one broadcast row (token stride 0) has no TMA view: such a
+// call, which has no use of its own, takes the kernels of fp32.
+bool on_tensor_cores(const vdn_linear_cfg* c, std::initializer_list<const vdn_view*> inputs) {
+  if (c->dtype != VDN_BF16) return false;
+  for (const vdn_view* v : inputs)
+    if (c->tokens > 1 && v->token_stride == 0) return false;
+  return true;
+}
 
-// Whole heads as ranges where there are enough of them, or where a head is
-// short; else equal ranges, which costs the parts' kernel and the scan.
-LinPlan make_plan(const vdn_linear_cfg* c, int jobs) {
+// Ranges: whole heads, or equal parts of all heads' chunks, which cost a kernel for the parts' states (`walks` of them,
+// half of a job's work each) and the scan.  In chunks of one CTA, with the two kernels' launches worth about eight.
+LinPlan make_plan(const vdn_linear_cfg* c, int jobs, int walks, bool tc) {
   LinPlan pl;
-  pl.chunk = on_tensor_cores(c) ? kLinTcChunk : kLinSimtChunk;
+  pl.chunk = tc ? kLinTcChunk : kLinSimtChunk;
   pl.nc = std::max(1, (c->tokens + pl.chunk - 1) / pl.chunk);
-  const int heads = c->batch * c->heads;
-  pl.total = (long long)heads * pl.nc;
-  const int most = kLinSms * 2 / jobs;
-  pl.split = heads < most && pl.nc > 8;
-  pl.grid = pl.split ? (int)std::min<long long>(most, pl.total) : heads;
+  const long long heads = (long long)c->batch * c->heads;
+  pl.total = heads * pl.nc;
+  const int per_wave = kLinSms * (tc ? 1 : 2);
+  const long long whole = (heads * jobs + per_wave - 1) / per_wave * pl.nc;
+  const long long parts = (pl.total * (2 * jobs + walks) + 2 * per_wave - 1) / (2 * per_wave) + 8;
+  pl.split = parts < whole;
+  pl.grid = pl.split ? (int)std::min<long long>(per_wave / jobs, pl.total) : (int)heads;
   return pl;
 }
 
@@ -141,14 +151,24 @@ cudaError_t copy_states(const vdn_linear_cfg* c, float* dst, long long dst_strid
                            cudaMemcpyDeviceToDevice, st);
 }
 
-cudaError_t run(const vdn_linear_cfg* c, LinStateParams& sp, LinOutParams& op, cudaStream_t st) {
+// The launches of a call; the jobs and walks name its tensors by their place, inputs first.
+cudaError_t run(const vdn_linear_cfg* c, bool tc, std::initializer_list<const vdn_view*> inputs,
+                std::initializer_list<const vdn_view*> outputs, LinStateParams& sp, LinOutParams& op, cudaStream_t st) {
   const int fp32 = c->dtype == VDN_FP32, D = c->head_dim;
+  LinTcMaps maps;
+  if (tc) {
+    int i = 0;
+    for (const vdn_view* v : inputs)
+      if (!make_lin_map(&maps.m[i++], view(v), c->batch, c->tokens, c->heads, D, false)) return cudaErrorInvalidValue;
+    for (const vdn_view* v : outputs)
+      if (!make_lin_map(&maps.m[i++], view(v), c->batch, c->tokens, c->heads, D, true)) return cudaErrorInvalidValue;
+  }
   if (op.pl.split) {
-    cudaError_t e = launch_lin_states_simt(sp, D, fp32, st);
+    cudaError_t e = tc ? launch_lin_states_tc(maps, sp, st) : launch_lin_states_simt(sp, D, fp32, st);
     if (e == cudaSuccess) e = launch_lin_scan(sp, D, st);
     if (e != cudaSuccess) return e;
   }
-  return launch_lin_out_simt(op, D, fp32, st);
+  return tc ? launch_lin_out_tc(maps, op, st) : launch_lin_out_simt(op, D, fp32, st);
 }
 
 }  // namespace
@@ -162,7 +182,13 @@ vdn_status vdn_linear_validate(const vdn_linear_cfg* cfg) { return check_linear(
 
 size_t vdn_linear_workspace_bytes(const vdn_linear_cfg* cfg, int32_t backward) {
   if (check_linear(cfg) != VDN_OK) return 0;
-  return make_layout(cfg, make_plan(cfg, backward ? 3 : 1), backward ? 2 : 1, !backward).total;
+  // either form of the kernels may serve a bf16 call
+  size_t most = 0;
+  for (bool tc : {false, true}) {
+    const LinPlan pl = backward ? make_plan(cfg, 3, 2, tc) : make_plan(cfg, 1, 1, tc);
+    most = std::max(most, make_layout(cfg, pl, backward ? 2 : 1, !backward).total);
+  }
+  return most;
 }
 
 vdn_status vdn_linear_attn_fwd(const vdn_view* q, const vdn_view* k, const vdn_view* v, const vdn_view* out,
@@ -183,7 +209,8 @@ vdn_status vdn_linear_attn_fwd(const vdn_view* q, const vdn_view* k, const vdn_v
       if ((s = check_view(cfg, x, false)) != VDN_OK) return s;
     if ((s = check_view(cfg, out, true)) != VDN_OK) return s;
   }
-  const LinPlan pl = make_plan(cfg, 1);
+  const bool tc = cfg->tokens > 0 && on_tensor_cores(cfg, {q, k, v});
+  const LinPlan pl = make_plan(cfg, 1, 1, tc);
   const LinLayout l = make_layout(cfg, pl, 1, true);
   if ((s = check_ws(cfg, l.total)) != VDN_OK) return s;
   if (cfg->tokens == 0)
@@ -193,26 +220,26 @@ vdn_status vdn_linear_attn_fwd(const vdn_view* q, const vdn_view* k, const vdn_v
   LinStateParams sp;
   std::memset(&sp, 0, sizeof(sp));
   sp.pl = pl;
-  sp.B = cfg->batch, sp.N = cfg->tokens, sp.H = cfg->heads, sp.n_walks = 1;
+  sp.B = cfg->batch, sp.N = cfg->tokens, sp.H = cfg->heads, sp.d = cfg->head_dim, sp.n_walks = 1;
   sp.log_decay = cfg->log_decay;
   sp.lengths = cfg->lengths;
   sp.status = cfg->status_word ? cfg->status_word : ws<int>(cfg, 0);
   sp.record = ws<int>(cfg, 64);
-  sp.walk[0] = LinWalk{view(k), view(v), 0, ws(cfg, l.parts[0]), ws(cfg, l.s_in[0]),
+  sp.walk[0] = LinWalk{view(k), view(v), 1, 2, 0, ws(cfg, l.parts[0]), ws(cfg, l.s_in[0]),
                        cfg->state_in && cfg->state_out ? ws(cfg, l.s_head) : nullptr, cfg->state_in, in_stride, 1.f};
   LinOutParams op;
   std::memset(&op, 0, sizeof(op));
   op.pl = pl;
-  op.B = sp.B, op.N = sp.N, op.H = sp.H, op.n_jobs = 1;
+  op.B = sp.B, op.N = sp.N, op.H = sp.H, op.d = sp.d, op.n_jobs = 1;
   op.alpha = scale_of(cfg);
   op.log_decay = sp.log_decay;
   op.lengths = sp.lengths;
   op.status = sp.status;
   op.record = sp.record;
   op.inject_timeout = (cfg->debug_flags & VDN_INJECT_TIMEOUT) != 0;
-  op.job[0] = LinJob{view(q), view(k), view(v), view(out), 0, 0, cfg->state_in, in_stride, 1.f,
+  op.job[0] = LinJob{view(q), view(k), view(v), view(out), 0, 1, 2, 3, 0, 0, cfg->state_in, in_stride, 1.f,
                      sp.walk[0].s_in, sp.walk[0].s_head, cfg->state_out, out_stride, 1.f};
-  return cuda_status(run(cfg, sp, op, st));
+  return cuda_status(run(cfg, tc, {q, k, v}, {out}, sp, op, st));
 }
 
 vdn_status vdn_linear_attn_bwd(const vdn_view* q, const vdn_view* k, const vdn_view* v, const vdn_view* d_out,
@@ -238,7 +265,8 @@ vdn_status vdn_linear_attn_bwd(const vdn_view* q, const vdn_view* k, const vdn_v
     for (const vdn_view* x : {dq, dk, dv})
       if ((s = check_view(cfg, x, true)) != VDN_OK) return s;
   }
-  const LinPlan pl = make_plan(cfg, 3);
+  const bool tc = cfg->tokens > 0 && on_tensor_cores(cfg, {q, k, v, d_out});
+  const LinPlan pl = make_plan(cfg, 3, 2, tc);
   const LinLayout l = make_layout(cfg, pl, 2, false);
   if ((s = check_ws(cfg, l.total)) != VDN_OK) return s;
   if (cfg->tokens == 0)
@@ -249,32 +277,32 @@ vdn_status vdn_linear_attn_bwd(const vdn_view* q, const vdn_view* k, const vdn_v
   LinStateParams sp;
   std::memset(&sp, 0, sizeof(sp));
   sp.pl = pl;
-  sp.B = cfg->batch, sp.N = cfg->tokens, sp.H = cfg->heads, sp.n_walks = 2;
+  sp.B = cfg->batch, sp.N = cfg->tokens, sp.H = cfg->heads, sp.d = cfg->head_dim, sp.n_walks = 2;
   sp.log_decay = cfg->log_decay;
   sp.lengths = cfg->lengths;
   sp.status = cfg->status_word ? cfg->status_word : ws<int>(cfg, 0);
   sp.record = ws<int>(cfg, 64);
-  sp.walk[0] = LinWalk{view(k), view(v), 0, ws(cfg, l.parts[0]), ws(cfg, l.s_in[0]), nullptr,
+  sp.walk[0] = LinWalk{view(k), view(v), 1, 2, 0, ws(cfg, l.parts[0]), ws(cfg, l.s_in[0]), nullptr,
                        cfg->state_in, in_stride, 1.f};
-  sp.walk[1] = LinWalk{view(q), view(d_out), 1, ws(cfg, l.parts[1]), ws(cfg, l.s_in[1]), nullptr,
+  sp.walk[1] = LinWalk{view(q), view(d_out), 0, 3, 1, ws(cfg, l.parts[1]), ws(cfg, l.s_in[1]), nullptr,
                        cfg->d_state_out, dout_stride, 1.f / alpha};
   LinOutParams op;
   std::memset(&op, 0, sizeof(op));
   op.pl = pl;
-  op.B = sp.B, op.N = sp.N, op.H = sp.H, op.n_jobs = 3;
+  op.B = sp.B, op.N = sp.N, op.H = sp.H, op.d = sp.d, op.n_jobs = 3;
   op.alpha = alpha;
   op.log_decay = sp.log_decay;
   op.lengths = sp.lengths;
   op.status = sp.status;
   op.record = sp.record;
   op.inject_timeout = (cfg->debug_flags & VDN_INJECT_TIMEOUT) != 0;
-  op.job[0] = LinJob{view(d_out), view(v), view(k), view(dq), 0, 1, cfg->state_in, in_stride, 1.f,
+  op.job[0] = LinJob{view(d_out), view(v), view(k), view(dq), 3, 2, 1, 4, 0, 1, cfg->state_in, in_stride, 1.f,
                      sp.walk[0].s_in, nullptr, nullptr, 0, 0.f};
-  op.job[1] = LinJob{view(v), view(d_out), view(q), view(dk), 1, 1, cfg->d_state_out, dout_stride, 1.f / alpha,
+  op.job[1] = LinJob{view(v), view(d_out), view(q), view(dk), 2, 3, 0, 5, 1, 1, cfg->d_state_out, dout_stride, 1.f / alpha,
                      sp.walk[1].s_in, nullptr, nullptr, 0, 0.f};
-  op.job[2] = LinJob{view(k), view(q), view(d_out), view(dv), 1, 0, cfg->d_state_out, dout_stride, 1.f / alpha,
+  op.job[2] = LinJob{view(k), view(q), view(d_out), view(dv), 1, 0, 3, 6, 1, 0, cfg->d_state_out, dout_stride, 1.f / alpha,
                      sp.walk[1].s_in, nullptr, cfg->d_state_in, din_stride, alpha};
-  return cuda_status(run(cfg, sp, op, st));
+  return cuda_status(run(cfg, tc, {q, k, v, d_out}, {dq, dk, dv}, sp, op, st));
 }
 
 vdn_status vdn_linear_attn_step(const vdn_view* q, const vdn_view* k, const vdn_view* v, const vdn_view* out,

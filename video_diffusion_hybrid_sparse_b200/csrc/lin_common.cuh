@@ -21,6 +21,11 @@ __device__ __forceinline__ int lin_length(const int* lengths, int b, int N) {
   return lengths ? min(max(lengths[b], 0), N) : N;
 }
 
+// Chunks before the end of a walk beyond which a token's decay to that end is 0 in fp32 (2^-150 and less).
+__device__ __forceinline__ int lin_horizon(float log2_decay, int chunk) {
+  return log2_decay < 0.f ? (int)fminf(160.f / -log2_decay / (float)chunk, 1e9f) + 2 : 1 << 30;
+}
+
 // A stretch of one CTA's range inside one head: chunks [u0, u1) in walk order.
 struct LinPiece {
   int bh, u0, u1;

@@ -260,37 +260,42 @@ __global__ void __launch_bounds__(kThreads) lin_out_simt(const __grid_constant__
 
 // State before each range that begins inside a head: s_in[j] = lambda^rows(j - 1)
 // s_in[j - 1] + part[j - 1] along the head's ranges, from the state before the
-// walk.  One thread owns four elements and goes through the ranges; the parts'
-// loads do not depend on one another.
-__global__ void lin_scan(const __grid_constant__ LinStateParams p, int DD) {
+// walk.  A thread owns two elements and goes through the ranges.  Bound by the
+// latency of its loads, which do not depend on one another: 16 are in flight.
+__global__ void __launch_bounds__(128) lin_scan(const __grid_constant__ LinStateParams p, int DD) {
+  constexpr int kAhead = 16;
   const LinPlan& pl = p.pl;
   const LinWalk& wk = p.walk[blockIdx.y];
-  const int per = (DD + 4 * (int)blockDim.x - 1) / (4 * (int)blockDim.x);  // blocks of a head
+  const int per = DD / (2 * (int)blockDim.x);  // blocks of a head
   const int bh = blockIdx.x / per, b = bh / p.H, h = bh % p.H;
   const long long head0 = (long long)bh * pl.nc;
   const int j0 = pl.range_of(head0), j1 = pl.range_of(head0 + pl.nc - 1);
-  const int e = (blockIdx.x % per * blockDim.x + threadIdx.x) * 4;
-  if (j1 == j0 || e >= DD) return;
+  if (j1 == j0) return;
+  const int e = (blockIdx.x % per * blockDim.x + threadIdx.x) * 2;
   const int len = lin_length(p.lengths, b, p.N);
   const float l2 = lin_log2_decay(p.log_decay[h]);
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  float2 s = make_float2(0.f, 0.f);
   if (wk.init) {
-    s = *reinterpret_cast<const float4*>(wk.init + b * wk.init_stride + (long long)h * DD + e);
+    s = *reinterpret_cast<const float2*>(wk.init + b * wk.init_stride + (long long)h * DD + e);
     s.x *= wk.init_mul;
     s.y *= wk.init_mul;
-    s.z *= wk.init_mul;
-    s.w *= wk.init_mul;
   }
-  if (wk.s_head) *reinterpret_cast<float4*>(wk.s_head + (long long)j0 * DD + e) = s;
+  if (wk.s_head) *reinterpret_cast<float2*>(wk.s_head + (long long)j0 * DD + e) = s;
   int u = 0;
-#pragma unroll 4
-  for (int j = j0 + 1; j <= j1; ++j) {
-    const int u_next = (int)(pl.start(j) - head0);
-    const float f = lin_pow(l2, lin_rows(u, u_next, len, pl, wk.reverse));
-    const float4 a = *reinterpret_cast<const float4*>(wk.parts + (long long)(j - 1) * DD + e);
-    s = make_float4(fmaf(f, s.x, a.x), fmaf(f, s.y, a.y), fmaf(f, s.z, a.z), fmaf(f, s.w, a.w));
-    *reinterpret_cast<float4*>(wk.s_in + (long long)j * DD + e) = s;
-    u = u_next;
+  for (int j = j0 + 1; j <= j1; j += kAhead) {
+    float2 a[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (j + i <= j1) a[i] = *reinterpret_cast<const float2*>(wk.parts + (long long)(j + i - 1) * DD + e);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (j + i <= j1) {
+        const int u_next = (int)(pl.start(j + i) - head0);
+        const float f = lin_pow(l2, lin_rows(u, u_next, len, pl, wk.reverse));
+        s = make_float2(fmaf(f, s.x, a[i].x), fmaf(f, s.y, a[i].y));
+        *reinterpret_cast<float2*>(wk.s_in + (long long)(j + i) * DD + e) = s;
+        u = u_next;
+      }
   }
 }
 
@@ -329,8 +334,7 @@ cudaError_t launch_lin_out_simt(const LinOutParams& p, int D, int fp32, cudaStre
 }
 
 cudaError_t launch_lin_scan(const LinStateParams& p, int D, cudaStream_t st) {
-  const int threads = 256;
-  lin_scan<<<dim3((D * D / 4 + threads - 1) / threads * p.B * p.H, p.n_walks), threads, 0, st>>>(p, D * D);
+  lin_scan<<<dim3(D * D / 256 * p.B * p.H, p.n_walks), 128, 0, st>>>(p, D * D);
   return cudaGetLastError();
 }
 

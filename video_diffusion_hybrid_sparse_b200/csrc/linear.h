@@ -32,13 +32,21 @@
 namespace vdn {
 
 constexpr int kLinSms = 148;          // CTAs a wave holds (one for each SM of a B200)
-constexpr int kLinMaxGrid = 2 * kLinSms;  // most ranges a walk is cut into
-constexpr int kLinSimtChunk = 32;     // rows of a chunk: fp32 kernels and head_dim 32
+constexpr int kLinSimtChunk = 32;     // rows of a chunk: fp32 kernels
 constexpr int kLinTcChunk = 128;      // rows of a chunk: tensor-core kernels
 
 struct LinView {
   void* p;
   long long sb, sn, sh;  // elements
+};
+
+// TMA view of a tensor; the coordinates of a broadcast dimension (or one of a single entry) are multiplied by 0.
+struct LinMap {
+  CUtensorMap map;
+  int mh, mb;
+};
+struct LinTcMaps {
+  LinMap m[7];  // the call's inputs, then its outputs
 };
 
 // The chunks of every (batch, head), (batch, head)-major and in walk order,
@@ -67,6 +75,7 @@ VDN_HD int lin_rows(int u0, int u1, int n, const LinPlan& pl, int reverse) {
 
 struct LinJob {
   LinView x, y, z, o;
+  int mx, my, mz, mo;    // x, y, z, o among the call's maps
   int reverse;
   int transposed;        // the states in memory are [z][y] for this job
   const float* init;     // state before the walk or null; entries init_stride apart, [H, D, D] each
@@ -82,7 +91,7 @@ struct LinJob {
 
 struct LinOutParams {
   LinPlan pl;
-  int B, N, H, n_jobs;
+  int B, N, H, d, n_jobs;
   float alpha;
   const float* log_decay;
   const int* lengths;
@@ -95,6 +104,7 @@ struct LinOutParams {
 // One walk's states: parts of the ranges, then their scan.
 struct LinWalk {
   LinView y, z;
+  int my, mz;
   int reverse;
   float* parts;        // [grid, D, D]
   float* s_in;         // [grid, D, D]
@@ -106,7 +116,7 @@ struct LinWalk {
 
 struct LinStateParams {
   LinPlan pl;
-  int B, N, H, n_walks;
+  int B, N, H, d, n_walks;
   const float* log_decay;
   const int* lengths;
   int* status;
@@ -128,6 +138,9 @@ struct LinStepParams {
 
 // fp32: 1 for fp32 tensors, 0 for bf16
 cudaError_t launch_lin_states_simt(const LinStateParams& p, int D, int fp32, cudaStream_t st);
+cudaError_t launch_lin_states_tc(const LinTcMaps& m, const LinStateParams& p, cudaStream_t st);
+cudaError_t launch_lin_out_tc(const LinTcMaps& m, const LinOutParams& p, cudaStream_t st);
+bool make_lin_map(LinMap* m, const LinView& v, int B, int N, int H, int d, bool output);
 cudaError_t launch_lin_scan(const LinStateParams& p, int D, cudaStream_t st);
 cudaError_t launch_lin_out_simt(const LinOutParams& p, int D, int fp32, cudaStream_t st);
 cudaError_t launch_lin_step(const LinStepParams& p, int D, int fp32, cudaStream_t st);
