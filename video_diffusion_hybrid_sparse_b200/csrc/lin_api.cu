@@ -98,6 +98,8 @@ LinPlan make_plan(const vdn_linear_cfg* c, int jobs, int walks, bool tc) {
   const long long parts = (pl.total * (2 * jobs + walks) + 2 * per_wave - 1) / (2 * per_wave) + 8;
   pl.split = parts < whole;
   pl.grid = pl.split ? (int)std::min<long long>(per_wave / jobs, pl.total) : (int)heads;
+  // a range's part in up to four pieces, of eight chunks at least
+  pl.sub = pl.split ? (int)std::max<long long>(1, std::min<long long>(kLinMaxSub, pl.total / pl.grid / 8)) : 1;
   return pl;
 }
 
@@ -108,10 +110,10 @@ struct LinLayout {
 LinLayout make_layout(const vdn_linear_cfg* c, const LinPlan& pl, int walks, bool head_copies) {
   LinLayout l;
   size_t off = 256;  // status slot: word 0 the status, the timeout record at byte 64
-  const size_t n = pl.split ? align_up((size_t)pl.grid * c->head_dim * c->head_dim * 4, 256) : 0;
+  const size_t n = pl.split ? align_up((size_t)pl.grid * c->head_dim * c->head_dim * 4, 256) : 0;  // a state of each range
   for (int i = 0; i < walks; ++i) {
     l.parts[i] = off;
-    off += n;
+    off += n * pl.sub;
     l.s_in[i] = off;
     off += n;
   }

@@ -37,4 +37,34 @@ struct LinPiece {
   }
 };
 
+// Chunks with real rows among [u0, u1), walk order.
+__device__ __forceinline__ void lin_real(int u0, int u1, int len, const LinPlan& pl, int reverse, int& a, int& b) {
+  const int n = (len + pl.chunk - 1) / pl.chunk;
+  a = reverse ? max(u0, pl.nc - n) : u0;
+  b = reverse ? u1 : min(u1, n);
+  if (a > b) a = b = u0;
+}
+
+// Range j's stretch (len: its head's tokens).
+__device__ __forceinline__ LinStretch lin_stretch(int j, int len, float log2_decay, const LinPlan& pl, int reverse) {
+  const long long t1 = pl.start(j + 1), head0 = (t1 - 1) / pl.nc * pl.nc, t0 = max(pl.start(j), head0);
+  LinStretch s;
+  s.bh = (int)(head0 / pl.nc);
+  if (t1 == head0 + pl.nc) {
+    s.u0 = s.u1 = s.end = 0;
+    return s;
+  }
+  lin_real((int)(t0 - head0), (int)(t1 - head0), len, pl, reverse, s.u0, s.u1);
+  s.u0 = max(s.u0, s.u1 - lin_horizon(log2_decay, pl.chunk));
+  s.end = s.u1;
+  return s;
+}
+// Its piece i of pl.sub.
+__device__ __forceinline__ LinStretch lin_piece_of(LinStretch s, int i, const LinPlan& pl) {
+  const int n = s.u1 - s.u0, u = s.u0;
+  s.u0 = u + n * i / pl.sub;
+  s.u1 = u + n * (i + 1) / pl.sub;
+  return s;
+}
+
 }  // namespace vdn

@@ -105,18 +105,14 @@ __global__ void __launch_bounds__(kThreads) lin_states_simt(const __grid_constan
   float *Y = sm, *Z = Y + L::kTile, *W = Z + L::kTile, *w = W + D * D;
   const LinPlan& pl = p.pl;
   const LinWalk& wk = p.walk[blockIdx.y];
-  const long long t1 = pl.start(blockIdx.x + 1);
-  // the last stretch of the range, if the head goes on behind it
-  const long long head0 = (t1 - 1) / pl.nc * pl.nc;
-  if (t1 == head0 + pl.nc) return;
-  const long long t0 = max(pl.start(blockIdx.x), head0);
-  const LinPiece pc(t0, t1, pl);
-  const int b = pc.bh / p.H, h = pc.bh % p.H, len = lin_length(p.lengths, b, p.N);
+  const int range = blockIdx.x / pl.sub;
+  const int bh = (int)((pl.start(range + 1) - 1) / pl.nc), b = bh / p.H, h = bh % p.H, len = lin_length(p.lengths, b, p.N);
   const float l2 = lin_log2_decay(p.log_decay[h]);
+  const LinStretch st = lin_piece_of(lin_stretch(range, len, l2, pl, wk.reverse), blockIdx.x % pl.sub, pl);
+  if (st.u0 == st.u1) return;
   for (int i = threadIdx.x; i < D * D; i += kThreads) W[i] = 0.f;
-  for (int u = pc.u0; u < pc.u1; ++u) {
+  for (int u = st.u0; u < st.u1; ++u) {
     const int row0 = (wk.reverse ? pl.nc - 1 - u : u) * kC, n = min(max(len - row0, 0), kC);
-    if (n == 0) continue;
     __syncthreads();
     load_rows<T, D>(Y, wk.y, b, h, row0, n);
     load_rows<T, D>(Z, wk.z, b, h, row0, n);
@@ -125,8 +121,9 @@ __global__ void __launch_bounds__(kThreads) lin_states_simt(const __grid_constan
     update_state<D>(W, Y, Z, w, lin_pow(l2, n), n);
   }
   __syncthreads();
+  const float left = lin_pow(l2, lin_rows(st.u1, st.end, len, pl, wk.reverse));  // decay to the stretch's end
   float* dst = wk.parts + (long long)blockIdx.x * D * D;
-  for (int i = threadIdx.x; i < D * D; i += kThreads) dst[i] = W[i];
+  for (int i = threadIdx.x; i < D * D; i += kThreads) dst[i] = left * W[i];
 }
 
 template <typename T, int D>
@@ -260,42 +257,55 @@ __global__ void __launch_bounds__(kThreads) lin_out_simt(const __grid_constant__
 
 // State before each range that begins inside a head: s_in[j] = lambda^rows(j - 1)
 // s_in[j - 1] + part[j - 1] along the head's ranges, from the state before the
-// walk.  A thread owns two elements and goes through the ranges.  Bound by the
-// latency of its loads, which do not depend on one another: 16 are in flight.
+// walk.  A thread owns four elements and goes through the ranges.  Bound by the
+// latency of its loads, which do not depend on one another: eight are in flight.
 __global__ void __launch_bounds__(128) lin_scan(const __grid_constant__ LinStateParams p, int DD) {
-  constexpr int kAhead = 16;
+  constexpr int kAhead = 8;
   const LinPlan& pl = p.pl;
   const LinWalk& wk = p.walk[blockIdx.y];
-  const int per = DD / (2 * (int)blockDim.x);  // blocks of a head
-  const int bh = blockIdx.x / per, b = bh / p.H, h = bh % p.H;
+  const int per = (DD + 4 * (int)blockDim.x - 1) / (4 * (int)blockDim.x);  // blocks of a head
+  const int bh = blockIdx.x / per, b = bh / p.H, h = bh % p.H, sub = pl.sub;
   const long long head0 = (long long)bh * pl.nc;
   const int j0 = pl.range_of(head0), j1 = pl.range_of(head0 + pl.nc - 1);
   if (j1 == j0) return;
-  const int e = (blockIdx.x % per * blockDim.x + threadIdx.x) * 2;
   const int len = lin_length(p.lengths, b, p.N);
   const float l2 = lin_log2_decay(p.log_decay[h]);
-  float2 s = make_float2(0.f, 0.f);
-  if (wk.init) {
-    s = *reinterpret_cast<const float2*>(wk.init + b * wk.init_stride + (long long)h * DD + e);
-    s.x *= wk.init_mul;
-    s.y *= wk.init_mul;
+  // the head's ranges j0 .. j1 - 1: decay over each, and whether the pieces of its part have been written
+  __shared__ float fall[kLinMaxGrid];
+  __shared__ bool has[kLinMaxGrid * kLinMaxSub];
+  const int n = (j1 - j0) * sub;
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const int j = j0 + i / sub;
+    const LinStretch st = lin_piece_of(lin_stretch(j, len, l2, pl, wk.reverse), i % sub, pl);
+    has[i] = st.u0 < st.u1;
+    if (i % sub == 0)
+      fall[i / sub] = lin_pow(l2, lin_rows((int)(max(pl.start(j), head0) - head0), (int)(pl.start(j + 1) - head0), len, pl, wk.reverse));
   }
-  if (wk.s_head) *reinterpret_cast<float2*>(wk.s_head + (long long)j0 * DD + e) = s;
-  int u = 0;
-  for (int j = j0 + 1; j <= j1; j += kAhead) {
-    float2 a[kAhead];
+  __syncthreads();
+  const int e = (blockIdx.x % per * blockDim.x + threadIdx.x) * 4;
+  if (e >= DD) return;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (wk.init) {
+    s = *reinterpret_cast<const float4*>(wk.init + b * wk.init_stride + (long long)h * DD + e);
+    s = make_float4(s.x * wk.init_mul, s.y * wk.init_mul, s.z * wk.init_mul, s.w * wk.init_mul);
+  }
+  if (wk.s_head) *reinterpret_cast<float4*>(wk.s_head + (long long)j0 * DD + e) = s;
+  for (int i0 = 0; i0 < n; i0 += kAhead) {
+    float4 a[kAhead];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      if (j + i <= j1) a[i] = *reinterpret_cast<const float2*>(wk.parts + (long long)(j + i - 1) * DD + e);
+    for (int i = 0; i < kAhead; ++i) {
+      a[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i0 + i < n && has[i0 + i])
+        a[i] = *reinterpret_cast<const float4*>(wk.parts + ((long long)j0 * sub + i0 + i) * DD + e);
+    }
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      if (j + i <= j1) {
-        const int u_next = (int)(pl.start(j + i) - head0);
-        const float f = lin_pow(l2, lin_rows(u, u_next, len, pl, wk.reverse));
-        s = make_float2(fmaf(f, s.x, a[i].x), fmaf(f, s.y, a[i].y));
-        *reinterpret_cast<float2*>(wk.s_in + (long long)(j + i) * DD + e) = s;
-        u = u_next;
-      }
+    for (int i = 0; i < kAhead; ++i) {
+      if (i0 + i >= n) continue;
+      const int k = (i0 + i) / sub;
+      if (i0 + i == k * sub) s = make_float4(fall[k] * s.x, fall[k] * s.y, fall[k] * s.z, fall[k] * s.w);
+      s = make_float4(s.x + a[i].x, s.y + a[i].y, s.z + a[i].z, s.w + a[i].w);
+      if (i0 + i == k * sub + sub - 1) *reinterpret_cast<float4*>(wk.s_in + (long long)(j0 + k + 1) * DD + e) = s;
+    }
   }
 }
 
@@ -306,7 +316,7 @@ cudaError_t states_simt(const LinStateParams& p, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(lin_states_simt<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        SimtLayout<D>::kBytes);
   if (e != cudaSuccess) return e;
-  lin_states_simt<T, D><<<dim3(p.pl.grid, p.n_walks), kThreads, SimtLayout<D>::kBytes, st>>>(p);
+  lin_states_simt<T, D><<<dim3(p.pl.grid * p.pl.sub, p.n_walks), kThreads, SimtLayout<D>::kBytes, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -334,7 +344,7 @@ cudaError_t launch_lin_out_simt(const LinOutParams& p, int D, int fp32, cudaStre
 }
 
 cudaError_t launch_lin_scan(const LinStateParams& p, int D, cudaStream_t st) {
-  lin_scan<<<dim3(D * D / 256 * p.B * p.H, p.n_walks), 128, 0, st>>>(p, D * D);
+  lin_scan<<<dim3((D * D + 511) / 512 * p.B * p.H, p.n_walks), 128, 0, st>>>(p, D * D);
   return cudaGetLastError();
 }
 

@@ -17,13 +17,13 @@
 // Bound by memory: a chunk reads three tiles and writes one (128 KB at
 // head_dim 128: 2.9 us of a 148th of the HBM rate) against 2560 cycles of
 // products; TMA keeps the next chunk's tiles in flight in a ring of slots.
-// Roles (28 warps): warp 0 TMA, warp 1 issues the products, warps 4-19 decay
+// Roles (28 warps): warp 0 TMA, warps 1-2 issue the products, warps 4-19 decay
 // (P in TMEM, then Y: its first part in place, the others beside), warps 20-27
 // write the output rows and carry W (a thread owns half a row of W).  TMEM is
 // full: S | O1 | O2 | dW, 128 columns each; P overwrites S's columns in place.
-// Order of a chunk's products: P Z, the next chunk's scores, X W, dW: W of this
-// chunk is published while P Z and the scores run, Y decayed while all three
-// do, and the next P made during dW.
+// Two warps issue, P Z and the next chunk's scores in turn, X W and dW in turn:
+// W of this chunk is published while P Z and the scores run, Y decayed while
+// all three do, and the next P made during dW.
 //
 // Products of 128 x 128 x 16 from shared memory take all its bandwidth (8 KB in
 // 64 cycles), so that every other access lengthens the chunk: arrivals are one
@@ -38,7 +38,7 @@
 //
 // head_dim 32 takes the 64-column form: TMA fills the upper columns with
 // zeros, so that DRAM traffic stays that of 32.
-#include <mutex>
+#include <algorithm>
 
 #include "lin_common.cuh"
 #include "sm100.cuh"
@@ -72,14 +72,6 @@ constexpr uint32_t kCtlRegs = 56, kDecayRegs = 48, kOutRegs = 128, kTcRegs = 72;
 static_assert(128 * kCtlRegs + kDecay * kDecayRegs + kOut * kOutRegs <= kTcThreads * kTcRegs, "registers of a CTA");
 
 constexpr uint32_t kColS = 0, kColO1 = 128, kColO2 = 256, kColDw = 384;
-
-// chunks with real rows among [pc.u0, pc.u1), walk order
-__device__ __forceinline__ void real_chunks(const LinPiece& pc, int len, int nc, int reverse, int& a, int& b) {
-  const int n = (len + kChunk - 1) / kChunk;
-  a = reverse ? max(pc.u0, nc - n) : pc.u0;
-  b = reverse ? pc.u1 : min(pc.u1, n);
-  if (a > b) a = b = pc.u0;
-}
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int h, int n, int b) {
   asm volatile(
@@ -309,18 +301,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) lin_out_tc(const __grid_constan
   if (threadIdx.x == 0) {
     for (int s = 0; s < L::kSlots; ++s) {
       mbar_init(&bars[kFull + s], 1);
-      mbar_init(&bars[kEmpty + s], 1);
+      mbar_init(&bars[kEmpty + s], 2);  // both issuing warps
     }
     mbar_init(&bars[kSFull], 1);
     mbar_init(&bars[kPReady], kDecay / 32);
     mbar_init(&bars[kYReady], kDecay / 32);
     mbar_init(&bars[kYFree], 1);
     mbar_init(&bars[kYReady2], kDecay / 32);
-    mbar_init(&bars[kOFull], 1);
+    mbar_init(&bars[kOFull], 2);
     mbar_init(&bars[kOFree], kOut / 32);
     mbar_init(&bars[kDwFull], 1);
     mbar_init(&bars[kWReady], kOut / 32);
-    mbar_init(&bars[kDone], 1);
+    mbar_init(&bars[kDone], 2);
     ab->given_up = 0;
     fence_mbar_init();
   }
@@ -349,7 +341,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lin_out_tc(const __grid_constan
         t += pc.u1 - pc.u0;
         const int b = pc.bh / p.H, h = pc.bh % p.H;
         int ua, ub;
-        real_chunks(pc, lin_length(p.lengths, b, p.N), pl.nc, rev, ua, ub);
+        lin_real(pc.u0, pc.u1, lin_length(p.lengths, b, p.N), pl, rev, ua, ub);
         for (int u = ua; u < ub && ok; ++u) {
           const int row = (rev ? pl.nc - 1 - u : u) * kChunk;
 #pragma unroll
@@ -367,16 +359,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) lin_out_tc(const __grid_constan
       if (!ok)
         for (int k = (i > L::kSlots ? i - L::kSlots : 0); k < i; ++k)
           mbar_drain(&bars[kFull + k % L::kSlots], (k / L::kSlots) & 1);
-    } else if (warp == 1) {
+    } else if (warp == 1 || warp == 2) {
       // ------------------------------------------------------------ products
-      // The whole warp goes through the loop and one lane issues: operands of warp-uniform code are made in uniform
-      // registers, which a product takes.
+      // Warp 1: scores and P Z; warp 2: X W and dW, so that one's waits pass while the other's products run.  The whole warp
+      // goes through the loop and one lane issues: operands of warp-uniform code are made in uniform registers, which a
+      // product takes.
       int total = 0;
       for (long long t = t_begin; t < t_end;) {
         const LinPiece pc(t, t_end, pl);
         t += pc.u1 - pc.u0;
         int ua, ub;
-        real_chunks(pc, lin_length(p.lengths, pc.bh / p.H, p.N), pl.nc, rev, ua, ub);
+        lin_real(pc.u0, pc.u1, lin_length(p.lengths, pc.bh / p.H, p.N), pl, rev, ua, ub);
         total += ub - ua;
       }
       constexpr uint32_t id_s = idesc_bf16_f32(128, kChunk, 0, 0), id_o = idesc_bf16_f32(128, D, 0, 1);
@@ -389,55 +382,68 @@ __global__ void __launch_bounds__(kTcThreads, 1) lin_out_tc(const __grid_constan
         return got;
       };
       auto loaded = [&](int t) { return wait(&bars[kFull + slot(t)], (t / L::kSlots) & 1); };
-      auto scores = [&](int c) {
-        if (!loaded(3 * c) || !loaded(3 * c + 1)) return false;
-        if (elect_one()) {
-          mma_columns<D, false>(tmem + kColS, tile(3 * c), tile(3 * c + 1), id_s);
-          mma_commit(&bars[kSFull]);
-        }
-        __syncwarp();
-        return true;
-      };
-      // failure-path test: wait, with a short limit, for a phase that only this warp's own commit completes
-      bool ok = !(p.inject_timeout && blockIdx.x == 0 && !wait(&bars[kSFull], 0, 10000000ll));
-      if (total > 0) ok = ok && scores(0);
-      for (int c = 0; c < total && ok; ++c) {
-        const uint32_t ph = c & 1;
-        const uint32_t y = tile(3 * c + 1), z = tile(3 * c + 2);
-        if (!loaded(3 * c + 2) || !wait(&bars[kPReady], ph)) break;
-        const int n_parts = parts_of[ph];  // as the decay warps have decided
-        if (c > 0 && !wait(&bars[kOFree], ph ^ 1)) break;
-        if (elect_one()) {
-          uint64_t dz = smem_desc(z, kChunk * 128, 1024, kLayoutSw128);
+      if (warp == 1) {
+        // failure-path test: wait, with a short limit, for a phase that only this warp's own commit completes
+        bool ok = !(p.inject_timeout && blockIdx.x == 0 && !wait(&bars[kSFull], 0, 10000000ll));
+        for (int c = -1; c < total && ok; ++c) {
+          const uint32_t ph = c & 1;
+          if (c >= 0) {
+            if (!loaded(3 * c + 2) || !wait(&bars[kPReady], ph)) break;
+            if (c > 0 && !wait(&bars[kOFree], ph ^ 1)) break;
+            if (elect_one()) {
+              uint64_t dz = smem_desc(tile(3 * c + 2), kChunk * 128, 1024, kLayoutSw128);
 #pragma unroll 1
-          for (int kk = 0; kk < kChunk / 16; ++kk, dz += 128)
-            mma_ts(tmem + kColO1, tmem + kColS + (kk >> 1) * 32 + (kk & 1) * 8, dz, id_o, kk > 0);
+              for (int kk = 0; kk < kChunk / 16; ++kk, dz += 128)
+                mma_ts(tmem + kColO1, tmem + kColS + (kk >> 1) * 32 + (kk & 1) * 8, dz, id_o, kk > 0);
+              mma_commit(&bars[kOFull]);
+              mma_commit(&bars[kEmpty + slot(3 * c + 2)]);
+            }
+            __syncwarp();
+          }
+          if (c + 1 == total) break;
+          const int t = 3 * (c + 1);
+          if (!loaded(t) || !loaded(t + 1)) break;
+          if (elect_one()) {
+            mma_columns<D, false>(tmem + kColS, tile(t), tile(t + 1), id_s);
+            mma_commit(&bars[kSFull]);
+            mma_commit(&bars[kEmpty + slot(t)]);
+            mma_commit(&bars[kEmpty + slot(t + 1)]);
+          }
+          __syncwarp();
         }
-        __syncwarp();
-        // the next scores before this state: the decay warps get on with them
-        if (c + 1 < total && !scores(c + 1)) break;
-        if (!wait(&bars[kWReady], ph)) break;
-        if (elect_one()) {
-          mma_columns<D, true>(tmem + kColO2, tile(3 * c), fresh(base) + L::kW, id_o);
-          mma_commit(&bars[kOFull]);
-          mma_commit(&bars[kEmpty + slot(3 * c)]);
+      } else {
+        for (int c = 0; c < total; ++c) {
+          const uint32_t ph = c & 1;
+          if (!loaded(3 * c) || !wait(&bars[kWReady], ph)) break;
+          if (c > 0 && !wait(&bars[kOFree], ph ^ 1)) break;
+          if (elect_one()) {
+            mma_columns<D, true>(tmem + kColO2, tile(3 * c), fresh(base) + L::kW, id_o);
+            mma_commit(&bars[kOFull]);
+            mma_commit(&bars[kEmpty + slot(3 * c)]);
+          }
+          __syncwarp();
+          const uint32_t y = tile(3 * c + 1), z = tile(3 * c + 2);
+          if (!loaded(3 * c + 2) || !wait(&bars[kYReady], ph)) break;
+          const int n_parts = parts_of[ph];  // as the decay warps have decided
+          if (n_parts == 3) {
+            if (elect_one()) {
+              mma_state<D>(tmem + kColDw, y, fresh(base) + L::kLo, fresh(base) + L::kZero, z, 0, 3);
+              mma_commit(&bars[kYFree]);
+            }
+            __syncwarp();
+          }
+          if (!wait(&bars[kYReady2], ph)) break;
+          if (elect_one()) {
+            if (n_parts == 2) mma_state<D>(tmem + kColDw, y, fresh(base) + L::kLo, fresh(base) + L::kZero, z, 0, 2);
+            mma_state<D>(tmem + kColDw, y + kHalf * 128, fresh(base) + L::kLo + (n_parts == 2 ? kHalf * D * 2 : 0),
+                         fresh(base) + L::kZero, z + kHalf * 128, 1, n_parts);
+            if (n_parts == 2) mma_commit(&bars[kYFree]);
+            mma_commit(&bars[kEmpty + slot(3 * c + 1)]);
+            mma_commit(&bars[kEmpty + slot(3 * c + 2)]);
+            mma_commit(&bars[kDwFull]);
+          }
+          __syncwarp();
         }
-        __syncwarp();
-        if (!wait(&bars[kYReady], ph)) break;
-        if (elect_one()) {
-          mma_state<D>(tmem + kColDw, y, fresh(base) + L::kLo, fresh(base) + L::kZero, z, 0, n_parts);
-          mma_commit(&bars[kYFree]);
-        }
-        __syncwarp();
-        if (!wait(&bars[kYReady2], ph)) break;
-        if (elect_one()) {
-          mma_state<D>(tmem + kColDw, y + kHalf * 128, fresh(base) + L::kLo + (n_parts == 2 ? kHalf * D * 2 : 0),
-                       fresh(base) + L::kZero, z + kHalf * 128, 1, n_parts);
-          mma_commit(&bars[kEmpty + slot(3 * c + 1)]);
-          mma_commit(&bars[kEmpty + slot(3 * c + 2)]);
-          mma_commit(&bars[kDwFull]);
-        }
-        __syncwarp();
       }
       // every product of this warp completes before TMEM is released
       if (elect_one()) mma_commit(&bars[kDone]);
@@ -456,7 +462,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lin_out_tc(const __grid_constan
       t += pc.u1 - pc.u0;
       const int b = pc.bh / p.H, h = pc.bh % p.H, len = lin_length(p.lengths, b, p.N);
       int ua, ub;
-      real_chunks(pc, len, pl.nc, rev, ua, ub);
+      lin_real(pc.u0, pc.u1, len, pl, rev, ua, ub);
       if (ua == ub) continue;
       const float l2 = lin_log2_decay(p.log_decay[h]);
       // Every warp writes the same table.  One that is ahead fills the other: it has passed a chunk of this piece, which
@@ -578,7 +584,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lin_out_tc(const __grid_constan
       t += pc.u1 - pc.u0;
       const int b = pc.bh / p.H, h = pc.bh % p.H, len = lin_length(p.lengths, b, p.N);
       int ua, ub;
-      real_chunks(pc, len, pl.nc, rev, ua, ub);
+      lin_real(pc.u0, pc.u1, len, pl, rev, ua, ub);
       const float l2 = lin_log2_decay(p.log_decay[h]);
       __nv_bfloat16* o = out_base + b * jb.o.sb + h * jb.o.sh + z0;
       // chunks behind the sequence
@@ -714,21 +720,48 @@ template <int D>
 struct StLayout {
   static constexpr int kTile = kChunk * D * 2;
   static constexpr int kSlots = D == 128 ? 5 : 8;
-  static constexpr int kLo = kSlots * kTile;  // second and third parts of a tile's halves
+  static constexpr int kLo = kSlots * kTile;  // two tiles of parts
+  // Second part of half `a` of chunk c: in one of the tiles, in turn; with a third part behind it, in tile a.
+  static __device__ __forceinline__ int parts(int c, int a, bool third) {
+    return third ? kLo + a * kTile : kLo + (c & 1) * kTile + a * kHalf * D * 2;
+  }
   static constexpr int kZero = kLo + 2 * kTile;
   static constexpr int kBar = kZero + (D == 64 ? 2048 : 0);
   static constexpr int kBytes = kBar + 288 + 1024;
 };
 static_assert(StLayout<128>::kBytes <= 232448 && StLayout<64>::kBytes <= 232448, "shared memory of an SM");
-enum { sFull = 0, sEmpty = 8, sReady = 16, sLoFree = 18, sDone = 20, sNumBars = 21 };
-constexpr int kStWorkers = 512;  // warps 2-17
-constexpr int kStThreads = 64 + kStWorkers;
+enum { sFull = 0, sEmpty = 8, sReady = 16, sLoFree = 18, sAccFull = 20, sAccFree = 22, sDone = 24, sNumBars };
+static_assert(sNumBars * 8 + 8 + sizeof(WaitRecord) <= 272, "barrier block");
+constexpr int kStWorkers = 512;  // decay warps 2-17
+constexpr int kStThreads = 64 + kStWorkers + 128;
+
+// One of the pieces that a CTA of the ranges' states goes through.
+struct StPiece {
+  int range, h, b, len, rev, u0, u1, end;
+  float l2;
+  const LinWalk* wk;
+  __device__ __forceinline__ StPiece(int i, const LinStateParams& p) {
+    const LinPlan& pl = p.pl;
+    wk = &p.walk[i % p.n_walks];
+    i /= p.n_walks;
+    range = i / pl.sub;
+    rev = wk->reverse;
+    const int bh = (int)((pl.start(range + 1) - 1) / pl.nc);
+    b = bh / p.H, h = bh % p.H;
+    len = lin_length(p.lengths, b, p.N);
+    l2 = lin_log2_decay(p.log_decay[h]);
+    const LinStretch st = lin_piece_of(lin_stretch(range, len, l2, pl, rev), i % pl.sub, pl);
+    u0 = st.u0, u1 = st.u1, end = st.end;
+  }
+};
 
 }  // namespace
 
-// part = sum over the last stretch of a range, if its head goes on behind it, of the rows' w y^T z, w the decay to the
-// range's end.  A chunk whose decay to there is below fp32's range adds nothing and is not read: a head that forgets
-// within some hundred tokens costs a few chunks, whatever the range.  Two tiles a chunk (64 KB at head_dim 128).
+// part = sum over a range's stretch (linear.h) of the rows' w y^T z, w the decay to the stretch's end, in pieces.  A chunk
+// whose decay to there is below fp32's range adds nothing and is not read: a head that forgets within some hundred tokens
+// costs a few chunks, whatever the range.  A CTA goes through pieces gridDim apart, so that heads share the SMs evenly;
+// loads run ahead into the next piece, and two accumulators let its products start while warps 18-21 read the last one
+// out.  Two tiles a chunk (64 KB at head_dim 128).
 template <int D>
 __global__ void __launch_bounds__(kStThreads, 1) lin_states_tc(const __grid_constant__ LinTcMaps maps,
                                                                const __grid_constant__ LinStateParams p) {
@@ -739,17 +772,7 @@ __global__ void __launch_bounds__(kStThreads, 1) lin_states_tc(const __grid_cons
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kBar + sNumBars * 8);
   WaitRecord* ab = reinterpret_cast<WaitRecord*>(smem + L::kBar + sNumBars * 8 + 8);
   const LinPlan& pl = p.pl;
-  const LinWalk& wk = p.walk[blockIdx.x % p.n_walks];
-  const int range = blockIdx.x / p.n_walks, rev = wk.reverse, d = D == 128 ? 128 : p.d;
-  const long long t1 = pl.start(range + 1);
-  const long long head0 = (t1 - 1) / pl.nc * pl.nc;
-  if (t1 == head0 + pl.nc) return;
-  const LinPiece pc(max(pl.start(range), head0), t1, pl);
-  const int b = pc.bh / p.H, h = pc.bh % p.H, len = lin_length(p.lengths, b, p.N);
-  const float l2 = lin_log2_decay(p.log_decay[h]);
-  int ua, ub;
-  real_chunks(pc, len, pl.nc, rev, ua, ub);
-  ua = max(ua, ub - lin_horizon(l2, kChunk));
+  const int n_pieces = p.n_walks * pl.grid * pl.sub;
   const uint32_t warp = warp_id(), lane = lane_id();
 
   if (threadIdx.x == 0) {
@@ -760,6 +783,8 @@ __global__ void __launch_bounds__(kStThreads, 1) lin_states_tc(const __grid_cons
     for (int a = 0; a < 2; ++a) {
       mbar_init(&bars[sReady + a], kStWorkers / 32);
       mbar_init(&bars[sLoFree + a], 1);
+      mbar_init(&bars[sAccFull + a], 1);
+      mbar_init(&bars[sAccFree + a], 4);
     }
     mbar_init(&bars[sDone], 1);
     ab->given_up = 0;
@@ -770,7 +795,7 @@ __global__ void __launch_bounds__(kStThreads, 1) lin_states_tc(const __grid_cons
       reinterpret_cast<uint4*>(smem + L::kZero)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
   if (warp == 1) {
-    tmem_alloc(tmem_slot, 128);
+    tmem_alloc(tmem_slot, 256);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -782,17 +807,21 @@ __global__ void __launch_bounds__(kStThreads, 1) lin_states_tc(const __grid_cons
     if (lane == 0) {
       int i = 0;
       bool ok = true;
-      const MapRef my(maps.m[wk.my]), mz(maps.m[wk.mz]);
-      for (int u = ua; u < ub && ok; ++u) {
-        const int row = (rev ? pl.nc - 1 - u : u) * kChunk;
+      for (int k = blockIdx.x; k < n_pieces && ok; k += gridDim.x) {
+        const StPiece pc(k, p);
+        if (pc.u0 == pc.u1) continue;
+        const MapRef my(maps.m[pc.wk->my]), mz(maps.m[pc.wk->mz]);
+        for (int u = pc.u0; u < pc.u1 && ok; ++u) {
+          const int row = (pc.rev ? pl.nc - 1 - u : u) * kChunk;
 #pragma unroll
-        for (int k = 0; k < 2; ++k, ++i) {
-          const int s = i % L::kSlots;
-          if (!lin_wait(&bars[sEmpty + s], ((i / L::kSlots) & 1) ^ 1, ab)) {
-            ok = false;
-            break;
+          for (int j = 0; j < 2; ++j, ++i) {
+            const int s = i % L::kSlots;
+            if (!lin_wait(&bars[sEmpty + s], ((i / L::kSlots) & 1) ^ 1, ab)) {
+              ok = false;
+              break;
+            }
+            load_tile<D>(smem + s * L::kTile, j ? mz : my, &bars[sFull + s], pc.h, row, pc.b);
           }
-          load_tile<D>(smem + s * L::kTile, k ? mz : my, &bars[sFull + s], h, row, b);
         }
       }
       if (!ok)
@@ -807,70 +836,91 @@ __global__ void __launch_bounds__(kStThreads, 1) lin_states_tc(const __grid_cons
       return got;
     };
     bool ok = true;
-    for (int c = 0; c < ub - ua && ok; ++c) {
-      const int ty = 2 * c, tz = ty + 1;
-      const int n_parts = third_part(l2, lin_rows(ua + c + 1, ub, len, pl, rev)) ? 3 : 2;
-      if (!wait(&bars[sFull + tz % L::kSlots], (tz / L::kSlots) & 1)) break;
-      const uint32_t y = fresh(base) + ty % L::kSlots * L::kTile, z = fresh(base) + tz % L::kSlots * L::kTile;
-#pragma unroll 1
-      for (int a = 0; a < 2; ++a) {
-        if (!(ok = ok && wait(&bars[sReady + a], c & 1))) continue;
+    int c = 0, done = 0;  // chunks; pieces
+    for (int k = blockIdx.x; k < n_pieces && ok; k += gridDim.x) {
+      const StPiece pc(k, p);
+      if (pc.u0 == pc.u1) continue;
+      const int buf = done & 1;
+      if (done > 1 && !(ok = wait(&bars[sAccFree + buf], ((done >> 1) & 1) ^ 1))) break;
+      const uint32_t acc = tmem + buf * 128;
+      for (int u = pc.u0; u < pc.u1 && ok; ++u, ++c) {
+        const int ty = 2 * c, tz = ty + 1;
+        const int n_parts = third_part(pc.l2, lin_rows(u + 1, pc.end, pc.len, pl, pc.rev)) ? 3 : 2;
+        if (!(ok = wait(&bars[sFull + tz % L::kSlots], (tz / L::kSlots) & 1))) break;
+        if (!(ok = wait(&bars[sReady + (c & 1)], (c >> 1) & 1))) break;
+        const uint32_t y = fresh(base) + ty % L::kSlots * L::kTile, z = fresh(base) + tz % L::kSlots * L::kTile;
         if (elect_one()) {
-          mma_state<D>(tmem, y + a * kHalf * 128, fresh(base) + L::kLo + a * L::kTile, fresh(base) + L::kZero,
-                       z + a * kHalf * 128, c > 0 || a > 0, n_parts);
-          if (a == 1) {
-            mma_commit(&bars[sEmpty + ty % L::kSlots]);
-            mma_commit(&bars[sEmpty + tz % L::kSlots]);
-          }
-          mma_commit(&bars[sLoFree + a]);
+#pragma unroll 1
+          for (int a = 0; a < 2; ++a)
+            mma_state<D>(acc, y + a * kHalf * 128, fresh(base) + L::parts(c, a, n_parts == 3), fresh(base) + L::kZero,
+                         z + a * kHalf * 128, u > pc.u0 || a > 0, n_parts);
+          mma_commit(&bars[sEmpty + ty % L::kSlots]);
+          mma_commit(&bars[sEmpty + tz % L::kSlots]);
+          mma_commit(&bars[sLoFree + (c & 1)]);
+          if (u + 1 == pc.u1) mma_commit(&bars[sAccFull + buf]);
         }
         __syncwarp();
       }
+      ++done;
     }
     if (elect_one()) mma_commit(&bars[sDone]);
     __syncwarp();
-  } else {
+  } else if (warp < 2 + kStWorkers / 32) {
     const int tid = threadIdx.x - 64;
     bool ok = true;
-    for (int u = ua, c = 0; u < ub; ++u, ++c) {
-      const int row0 = (rev ? pl.nc - 1 - u : u) * kChunk, n = min(len - row0, kChunk);
-      const int ty = 2 * c, tz = ty + 1, more = lin_rows(u + 1, ub, len, pl, rev);
-      bool got = lin_wait(&bars[sFull + ty % L::kSlots], (ty / L::kSlots) & 1, ab);
-      if (got && n < kChunk) got = lin_wait(&bars[sFull + tz % L::kSlots], (tz / L::kSlots) & 1, ab);
-      if (__any_sync(0xffffffffu, !got)) { ok = false; break; }
-      if (n < kChunk) clear_rows<D, kStWorkers>(smem + tz % L::kSlots * L::kTile, tid, n);
+    int c = 0;
+    bool both = false;  // the chunk before takes both tiles of parts
+    for (int k = blockIdx.x; k < n_pieces && ok; k += gridDim.x) {
+      const StPiece pc(k, p);
+      for (int u = pc.u0; u < pc.u1; ++u, ++c) {
+        const int row0 = (pc.rev ? pl.nc - 1 - u : u) * kChunk, n = min(pc.len - row0, kChunk);
+        const int ty = 2 * c, tz = ty + 1, more = lin_rows(u + 1, pc.end, pc.len, pl, pc.rev);
+        bool got = lin_wait(&bars[sFull + ty % L::kSlots], (ty / L::kSlots) & 1, ab);
+        if (got && n < kChunk) got = lin_wait(&bars[sFull + tz % L::kSlots], (tz / L::kSlots) & 1, ab);
+        if (__any_sync(0xffffffffu, !got)) { ok = false; break; }
+        // the tiles of parts that this chunk takes are free: the products of the chunk before, or of the one before that
+        const bool third = third_part(pc.l2, more);
+        const int after = c - (third || both ? 1 : 2);
+        if (after >= 0 && __any_sync(0xffffffffu, !lin_wait(&bars[sLoFree + (after & 1)], (after >> 1) & 1, ab))) {
+          ok = false;
+          break;
+        }
+        both = third;
+        if (n < kChunk) clear_rows<D, kStWorkers>(smem + tz % L::kSlots * L::kTile, tid, n);
 #pragma unroll 1
-      for (int a = 0; a < 2; ++a) {
-        if (ok && c > 0 && __any_sync(0xffffffffu, !lin_wait(&bars[sLoFree + a], (c & 1) ^ 1, ab))) ok = false;
-        if (!ok) continue;
-        decay_half<D, kStWorkers>(smem + ty % L::kSlots * L::kTile, smem + L::kLo + a * L::kTile, a * kHalf, tid, l2, n, rev,
-                                  more, third_part(l2, more));
+        for (int a = 0; a < 2; ++a)
+          decay_half<D, kStWorkers>(smem + ty % L::kSlots * L::kTile, smem + L::parts(c, a, third), a * kHalf, tid, pc.l2, n,
+                                    pc.rev, more, third);
         fence_proxy_async_smem();
-        arrive_warp(&bars[sReady + a]);
+        arrive_warp(&bars[sReady + (c & 1)]);
       }
-      if (!ok) break;
     }
-    // read-out: a warp has 32 rows and a quarter of the columns
-    constexpr int kCols = D / 4;
-    const int q = warp & 3, r = q * 32 + lane, z0 = (warp - 2) / 4 * kCols;
-    if (ok && __any_sync(0xffffffffu, !lin_wait(&bars[sDone], 0, ab))) ok = false;
-    if (ok) {
+  } else {
+    // read-out of finished pieces: a thread has a row
+    const int q = warp & 3, r = q * 32 + lane, d = D == 128 ? 128 : p.d;
+    int done = 0;
+    for (int k = blockIdx.x; k < n_pieces; k += gridDim.x) {
+      const StPiece pc(k, p);
+      if (pc.u0 == pc.u1) continue;
+      const int buf = done & 1;
+      if (__any_sync(0xffffffffu, !lin_wait(&bars[sAccFull + buf], (done >> 1) & 1, ab))) break;
       tc_fence_after();
-      float* dst = wk.parts + (long long)range * d * d + (long long)r * d + z0;
-#pragma unroll
-      for (int e = 0; e < kCols; e += 16) {
+      float* dst = pc.wk->parts + (long long)(k / p.n_walks) * d * d + (long long)r * d;
+#pragma unroll 1
+      for (int e = 0; e < D; e += 16) {
         uint32_t x[16];
-        tmem_ld16(tmem_addr(tmem, q * 32, z0 + e), x);
+        tmem_ld16(tmem_addr(tmem + buf * 128, q * 32, e), x);
         tmem_wait_ld();
-        if (r < d && z0 < d) {
+        if (r < d && e < d) {
 #pragma unroll
-          for (int k = 0; k < 16; k += 4)
-            *reinterpret_cast<float4*>(dst + e + k) =
-                ua < ub ? make_float4(__uint_as_float(x[k]), __uint_as_float(x[k + 1]), __uint_as_float(x[k + 2]),
-                                      __uint_as_float(x[k + 3]))
-                        : make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int i = 0; i < 16; i += 4)
+            *reinterpret_cast<float4*>(dst + e + i) = make_float4(__uint_as_float(x[i]), __uint_as_float(x[i + 1]),
+                                                                  __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
         }
       }
+      tc_fence_before();
+      arrive_warp(&bars[sAccFree + buf]);
+      ++done;
     }
   }
   tc_fence_before();
@@ -879,7 +929,7 @@ __global__ void __launch_bounds__(kStThreads, 1) lin_states_tc(const __grid_cons
   if (threadIdx.x == 0) report(*ab, p.status, p.record, 21);
   if (warp == 1) {
     mbar_drain(&bars[sDone], 0);
-    tmem_dealloc(tmem, 128);
+    tmem_dealloc(tmem, 256);
   }
 }
 
@@ -902,7 +952,7 @@ template <int D>
 cudaError_t states_tc(const LinTcMaps& m, const LinStateParams& p, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(lin_states_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, StLayout<D>::kBytes);
   if (e != cudaSuccess) return e;
-  lin_states_tc<D><<<p.n_walks * p.pl.grid, kStThreads, StLayout<D>::kBytes, st>>>(m, p);
+  lin_states_tc<D><<<std::min(kLinSms, p.n_walks * p.pl.grid * p.pl.sub), kStThreads, StLayout<D>::kBytes, st>>>(m, p);
   return cudaGetLastError();
 }
 

@@ -32,6 +32,8 @@
 namespace vdn {
 
 constexpr int kLinSms = 148;          // CTAs a wave holds (one for each SM of a B200)
+constexpr int kLinMaxGrid = 2 * kLinSms;  // most ranges of a split plan
+constexpr int kLinMaxSub = 4;             // most pieces of a range's part
 constexpr int kLinSimtChunk = 32;     // rows of a chunk: fp32 kernels
 constexpr int kLinTcChunk = 128;      // rows of a chunk: tensor-core kernels
 
@@ -59,6 +61,7 @@ struct LinPlan {
   int nc;           // chunks of a head
   int grid;         // ranges
   int split;        // a range may begin inside a head
+  int sub;          // pieces of a range's part, each formed by a CTA of its own
   long long total;  // chunks of all heads
 
   VDN_HD long long start(int j) const { return total * j / grid; }
@@ -72,6 +75,12 @@ VDN_HD int lin_rows(int u0, int u1, int n, const LinPlan& pl, int reverse) {
   const long long most = (long long)(hi - lo) * pl.chunk, have = (long long)n - (long long)lo * pl.chunk;
   return (int)(have < 0 ? 0 : have < most ? have : most);
 }
+
+// The chunks that carry the part of range j (walk order): the range's last stretch, if its head goes on behind it, from
+// where a token's decay to the stretch's end is not 0 in fp32; piece i of it.  Empty: u0 == u1.
+struct LinStretch {
+  int bh, u0, u1, end;
+};
 
 struct LinJob {
   LinView x, y, z, o;
@@ -106,7 +115,7 @@ struct LinWalk {
   LinView y, z;
   int my, mz;
   int reverse;
-  float* parts;        // [grid, D, D]
+  float* parts;        // [grid, sub, D, D]; a piece without weight is not written
   float* s_in;         // [grid, D, D]
   float* s_head;       // [grid, D, D] or null (LinJob::s_head)
   const float* init;
