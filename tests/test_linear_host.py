@@ -173,3 +173,12 @@ def test_workspace_follows_the_split():
     assert vb.linear_workspace_bytes(64, 100_000, 16, 128) == 256
     with pytest.raises(vb.VdnError):
         vb.linear_workspace_bytes(1, 10, 1, 40)
+
+
+@pytest.mark.parametrize("struct,pack", [(vb.VdnView, vb._VIEW), (vb.VdnLinearCfg, vb._LINEAR), (vb.VdnNormCfg, vb._NORM)])
+def test_packed_forms_match_the_structures(struct, pack):
+    values = [i + 1 for i in range(len(struct._fields_))]
+    b = pack(*values)
+    assert len(b) == ctypes.sizeof(struct)
+    s = struct.from_buffer_copy(b)
+    assert [getattr(s, f[0]) for f in struct._fields_] == values

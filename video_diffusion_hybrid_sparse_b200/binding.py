@@ -9,7 +9,9 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
+import struct
 from dataclasses import dataclass
 
 import numpy as np
@@ -17,6 +19,7 @@ import torch
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libvdnattn.so")
 _lib = None
+_lib_packed = None
 
 VDN_BF16, VDN_FP32 = 0, 1
 OUT_SOFTMAX_ONLY, OUT_LINEAR_ONLY, OUT_LINEAR_RAW, EXPORT_STATES, INJECT_TIMEOUT = 1, 2, 4, 8, 16
@@ -136,6 +139,24 @@ def library() -> ctypes.CDLL:
                 getattr(lib, name).restype = ctypes.c_int
         _lib = lib
     return _lib
+
+
+def _packed() -> ctypes.CDLL:
+    """The calls of the linear memory and of the norm with views and configs as
+    packed bytes: filling a ctypes structure field by field takes longer than
+    the smallest of these calls run."""
+    global _lib_packed
+    if _lib_packed is None:
+        library()
+        lib = ctypes.CDLL(_LIB_PATH)
+        P, S = ctypes.c_void_p, ctypes.c_char_p
+        lib.vdn_linear_attn_fwd.argtypes = [S, S, S, S, S, P]
+        lib.vdn_linear_attn_bwd.argtypes = [S, S, S, S, S, S, S, S, P]
+        lib.vdn_linear_attn_step.argtypes = [S, S, S, S, S, P]
+        lib.vdn_add_rmsnorm_fwd.argtypes = [P, P, P, P, P, S, P]
+        lib.vdn_add_rmsnorm_bwd.argtypes = [P, P, P, P, P, S, P]
+        _lib_packed = lib
+    return _lib_packed
 
 
 @dataclass
@@ -463,6 +484,10 @@ def validate(s: Shape, **kw) -> int:
 NORM_OUT_TENSOR, NORM_OUT_E4M3_ROW, NORM_OUT_E4M3_GROUP = 0, 1, 2
 _DTYPES = {torch.bfloat16: VDN_BF16, torch.float32: VDN_FP32}
 _HERE = contextlib.nullcontext()
+# the fields of VdnView, VdnLinearCfg and VdnNormCfg in their order
+_VIEW = struct.Struct("@P3q").pack
+_LINEAR = struct.Struct("@5if6P4qP2iPNP").pack
+_NORM = struct.Struct("@q3if P7qPN").pack
 
 
 def _on(t: torch.Tensor, stream):
@@ -474,71 +499,68 @@ def _on(t: torch.Tensor, stream):
         if stream.device != t.device:
             raise ValueError("the stream and the tensors are on different devices")
         return torch.cuda.stream(stream)
-    return _HERE if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+    return _HERE if t.get_device() == torch.cuda.current_device() else torch.cuda.device(t.device)
 
 
-def _match(name, t, shape, dtype, device):
-    """``t`` has this shape, type and device and elements of its last dimension side by side."""
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device:
-        raise ValueError(f"{name}: expected {tuple(shape)} {dtype} on {device}, got {tuple(t.shape)} {t.dtype} "
-                         f"on {t.device}")
-    if len(shape) > 1 and t.stride(-1) != 1 and shape[-1] != 1:
+def _here(t: torch.Tensor) -> int:
+    """The current stream of the device of ``t``."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _match(name, t, like):
+    """``t`` has the shape, type and device of ``like``, and rows of contiguous elements."""
+    if t.shape != like.shape or t.dtype != like.dtype or t.device != like.device:
+        raise ValueError(f"{name}: expected {tuple(like.shape)} {like.dtype} on {like.device}, got {tuple(t.shape)} "
+                         f"{t.dtype} on {t.device}")
+    if t.stride(-1) != 1 and t.shape[-1] != 1:
         raise ValueError(f"{name}: the elements of the last dimension must be contiguous")
 
 
-def _view(t: torch.Tensor) -> VdnView:
-    """[B, N, H, d] or (a step's) [B, H, d]."""
+def _view(name, t, like) -> bytes:
+    """Packed view of a [B, N, H, d] or (a step's) [B, H, d] tensor, checked against ``like``."""
     s = t.stride()
-    return VdnView(t.data_ptr(), s[0], s[1], s[2]) if len(s) == 4 else VdnView(t.data_ptr(), s[0], 0, s[1])
+    if t.shape != like.shape or t.dtype != like.dtype or t.device != like.device or s[-1] != 1:
+        _match(name, t, like)
+    return _VIEW(t.data_ptr(), s[0], s[1], s[2]) if len(s) == 4 else _VIEW(t.data_ptr(), s[0], 0, s[1])
 
 
 def _state(name, t, B, H, d, device):
     """Pointer and batch stride of [B, H, d, d] fp32 states (the last three dimensions contiguous)."""
     if t is None:
-        return None, 0
-    if tuple(t.shape) != (B, H, d, d) or t.dtype != torch.float32 or t.device != device:
+        return 0, 0
+    if t.shape != (B, H, d, d) or t.dtype != torch.float32 or t.device != device:
         raise ValueError(f"{name}: expected {(B, H, d, d)} torch.float32 on {device}, got {tuple(t.shape)} {t.dtype} "
                          f"on {t.device}")
-    if t.stride()[1:] != (d * d, d, 1):
+    s = t.stride()
+    if s[1:] != (d * d, d, 1) and (H > 1 or s[2:] != (d, 1)):
         raise ValueError(f"{name}: the last three dimensions must be contiguous")
-    return t.data_ptr(), t.stride(0) if B > 1 else H * d * d
+    return t.data_ptr(), s[0] if B > 1 else 0
 
 
 def _flat(name, t, n, dtype, device):
-    """Pointer of a contiguous vector of n elements, or None."""
+    """Pointer of a contiguous vector of n elements, or 0."""
     if t is None:
-        return None
-    if tuple(t.shape) != (n,) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        return 0
+    if t.shape != (n,) or t.dtype != dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous ({n},) {dtype} on {device}, got {tuple(t.shape)} {t.dtype} "
                          f"on {t.device}")
     return t.data_ptr()
 
 
-def _linear_cfg(q, log_decay, scale, lengths, status, debug_flags) -> VdnLinearCfg:
-    if q.dim() != 4 or q.dtype not in _DTYPES:
-        raise ValueError(f"q: expected a [B, N, H, d] bf16 or fp32 tensor, got {tuple(q.shape)} {q.dtype}")
-    B, N, H, d = q.shape
-    cfg = VdnLinearCfg()
-    cfg.batch, cfg.tokens, cfg.heads, cfg.head_dim, cfg.dtype = B, N, H, d, _DTYPES[q.dtype]
-    cfg.scale = scale
-    cfg.log_decay = _flat("log_decay", log_decay, H, torch.float32, q.device)
-    cfg.lengths = _flat("lengths", lengths, B, torch.int32, q.device)
-    cfg.status_word = _ptr(status)
-    cfg.debug_flags = debug_flags
-    return cfg
+def _word(name, t, device):
+    """Pointer of an int32 status word, or 0."""
+    if t is None:
+        return 0
+    if t.numel() < 1 or t.dtype != torch.int32 or t.device != device:
+        raise ValueError(f"{name}: expected an int32 word on {device}, got {tuple(t.shape)} {t.dtype} on {t.device}")
+    return t.data_ptr()
 
 
-def _linear_workspace(cfg, backward, workspace, device):
-    """``workspace``, or a new one from the caching allocator: it belongs to the
-    current stream (and, during a capture, to that graph), so calls on several
-    streams and captured graphs share none."""
-    if workspace is None:
-        n = library().vdn_linear_workspace_bytes(ctypes.byref(cfg), backward)
-        if n == 0:
-            _check(library().vdn_linear_validate(ctypes.byref(cfg)), "vdn_linear_workspace_bytes")
-        workspace = torch.empty(n, dtype=torch.uint8, device=device)
-    cfg.workspace, cfg.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    return workspace
+def _sizes(q, dims):
+    if q.dim() != dims or q.dtype not in _DTYPES:
+        raise ValueError(f"q: expected a {'[B, N, H, d]' if dims == 4 else '[B, H, d]'} bf16 or fp32 tensor, got "
+                         f"{tuple(q.shape)} {q.dtype}")
+    return q.shape
 
 
 def linear_workspace_bytes(B: int, N: int, H: int, d: int, dtype=torch.bfloat16, backward: bool = False) -> int:
@@ -549,6 +571,21 @@ def linear_workspace_bytes(B: int, N: int, H: int, d: int, dtype=torch.bfloat16,
     if n == 0:
         _check(library().vdn_linear_validate(ctypes.byref(cfg)), "vdn_linear_workspace_bytes")
     return n
+
+
+# sizes only: nothing of a call's tensors
+_linear_bytes = functools.lru_cache(maxsize=256)(linear_workspace_bytes)
+
+
+def _scratch(workspace, n, device):
+    """``workspace``, or a new one of ``n`` bytes from the caching allocator: it
+    belongs to the current stream (and, during a capture, to that graph), so calls
+    on several streams and captured graphs share none."""
+    if workspace is None:
+        return torch.empty(n, dtype=torch.uint8, device=device)
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace: expected a contiguous tensor on {device}")
+    return workspace
 
 
 def linear_attn_fwd(q, k, v, log_decay, *, scale: float = 0.0, state_in=None, state_out=None, lengths=None, out=None,
@@ -564,20 +601,18 @@ def linear_attn_fwd(q, k, v, log_decay, *, scale: float = 0.0, state_in=None, st
     be state_in; lengths: [B] int32 or None, the tokens of each padded sequence:
     rows behind them come out as zeros.  ``scale`` <= 0 selects d**-0.5."""
     with _on(q, stream):
-        cfg = _linear_cfg(q, log_decay, scale, lengths, status, debug_flags)
-        B, N, H, d = q.shape
-        _match("q", q, q.shape, q.dtype, q.device)
-        _match("k", k, q.shape, q.dtype, q.device)
-        _match("v", v, q.shape, q.dtype, q.device)
+        B, N, H, d = _sizes(q, 4)
+        dev = q.device
         if out is None:
-            out = torch.empty((B, N, H, d), dtype=q.dtype, device=q.device)
-        else:
-            _match("out", out, q.shape, q.dtype, q.device)
-        cfg.state_in, cfg.state_in_stride = _state("state_in", state_in, B, H, d, q.device)
-        cfg.state_out, cfg.state_out_stride = _state("state_out", state_out, B, H, d, q.device)
-        workspace = _linear_workspace(cfg, 0, workspace, q.device)
-        code = library().vdn_linear_attn_fwd(_view(q), _view(k), _view(v), _view(out), ctypes.byref(cfg), _stream())
-        _check(code, "vdn_linear_attn_fwd")
+            out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        a, b, c, o = _view("q", q, q), _view("k", k, q), _view("v", v, q), _view("out", out, q)
+        s_in, s_in_stride = _state("state_in", state_in, B, H, d, dev)
+        s_out, s_out_stride = _state("state_out", state_out, B, H, d, dev)
+        ws = _scratch(workspace, _linear_bytes(B, N, H, d, q.dtype), dev)
+        cfg = _LINEAR(B, N, H, d, _DTYPES[q.dtype], scale, _flat("log_decay", log_decay, H, torch.float32, dev),
+                      _flat("lengths", lengths, B, torch.int32, dev), s_in, s_out, 0, 0, s_in_stride, s_out_stride, 0, 0,
+                      0, 0, debug_flags, ws.data_ptr(), ws.nbytes, _word("status", status, dev))
+        _check(_packed().vdn_linear_attn_fwd(a, b, c, o, cfg, _here(q)), "vdn_linear_attn_fwd")
     return out
 
 
@@ -590,25 +625,21 @@ def linear_attn_bwd(q, k, v, log_decay, d_out, *, scale: float = 0.0, state_in=N
     by state_in.  Nothing of the forward call is kept: q, k, v and state_in are
     read again.  Rows behind ``lengths`` get zeros."""
     with _on(q, stream):
-        cfg = _linear_cfg(q, log_decay, scale, lengths, status, debug_flags)
-        B, N, H, d = q.shape
-        for name, t in (("q", q), ("k", k), ("v", v), ("d_out", d_out)):
-            _match(name, t, q.shape, q.dtype, q.device)
-        grads = []
-        for name, t in (("dq", dq), ("dk", dk), ("dv", dv)):
-            if t is None:
-                t = torch.empty((B, N, H, d), dtype=q.dtype, device=q.device)
-            else:
-                _match(name, t, q.shape, q.dtype, q.device)
-            grads.append(t)
-        cfg.state_in, cfg.state_in_stride = _state("state_in", state_in, B, H, d, q.device)
-        cfg.d_state_out, cfg.d_state_out_stride = _state("d_state_out", d_state_out, B, H, d, q.device)
-        cfg.d_state_in, cfg.d_state_in_stride = _state("d_state_in", d_state_in, B, H, d, q.device)
-        workspace = _linear_workspace(cfg, 1, workspace, q.device)
-        code = library().vdn_linear_attn_bwd(_view(q), _view(k), _view(v), _view(d_out), *map(_view, grads),
-                                             ctypes.byref(cfg), _stream())
-        _check(code, "vdn_linear_attn_bwd")
-    return tuple(grads)
+        B, N, H, d = _sizes(q, 4)
+        dev = q.device
+        dq, dk, dv = (torch.empty(q.shape, dtype=q.dtype, device=dev) if t is None else t for t in (dq, dk, dv))
+        views = [_view(n, t, q) for n, t in (("q", q), ("k", k), ("v", v), ("d_out", d_out), ("dq", dq), ("dk", dk),
+                                             ("dv", dv))]
+        s_in, s_in_stride = _state("state_in", state_in, B, H, d, dev)
+        ds_out, ds_out_stride = _state("d_state_out", d_state_out, B, H, d, dev)
+        ds_in, ds_in_stride = _state("d_state_in", d_state_in, B, H, d, dev)
+        ws = _scratch(workspace, _linear_bytes(B, N, H, d, q.dtype, True), dev)
+        cfg = _LINEAR(B, N, H, d, _DTYPES[q.dtype], scale, _flat("log_decay", log_decay, H, torch.float32, dev),
+                      _flat("lengths", lengths, B, torch.int32, dev), s_in, 0, ds_out, ds_in, s_in_stride, 0,
+                      ds_out_stride, ds_in_stride, 0, 0, debug_flags, ws.data_ptr(), ws.nbytes,
+                      _word("status", status, dev))
+        _check(_packed().vdn_linear_attn_bwd(*views, cfg, _here(q)), "vdn_linear_attn_bwd")
+    return dq, dk, dv
 
 
 def linear_attn_step(q, k, v, log_decay, state, *, slots=None, scale: float = 0.0, out=None, status=None,
@@ -621,45 +652,51 @@ def linear_attn_step(q, k, v, log_decay, state, *, slots=None, scale: float = 0.
     touched), and so does one past the pool, which also sets ``status`` (int32) to
     1.  Rows of the same slot are successive tokens, in the order of the rows."""
     with _on(q, stream):
-        if q.dim() != 3 or q.dtype not in _DTYPES:
-            raise ValueError(f"q: expected a [B, H, d] bf16 or fp32 tensor, got {tuple(q.shape)} {q.dtype}")
-        B, H, d = q.shape
-        for name, t in (("q", q), ("k", k), ("v", v)):
-            _match(name, t, q.shape, q.dtype, q.device)
+        B, H, d = _sizes(q, 3)
+        dev = q.device
         if out is None:
-            out = torch.empty((B, H, d), dtype=q.dtype, device=q.device)
-        else:
-            _match("out", out, q.shape, q.dtype, q.device)
-        cfg = VdnLinearCfg()
-        cfg.batch, cfg.heads, cfg.head_dim, cfg.dtype, cfg.scale = B, H, d, _DTYPES[q.dtype], scale
-        cfg.log_decay = _flat("log_decay", log_decay, H, torch.float32, q.device)
-        cfg.state_out, cfg.state_out_stride = _state("state", state, state.shape[0], H, d, q.device)
-        cfg.slots, cfg.n_slots = _flat("slots", slots, B, torch.int32, q.device), state.shape[0]
-        cfg.status_word = _ptr(status)
-        code = library().vdn_linear_attn_step(_view(q), _view(k), _view(v), _view(out), ctypes.byref(cfg), _stream())
-        _check(code, "vdn_linear_attn_step")
+            out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        a, b, c, o = _view("q", q, q), _view("k", k, q), _view("v", v, q), _view("out", out, q)
+        n = state.shape[0]
+        pool, slot_stride = _state("state", state, n, H, d, dev)
+        cfg = _LINEAR(B, 0, H, d, _DTYPES[q.dtype], scale, _flat("log_decay", log_decay, H, torch.float32, dev), 0, 0,
+                      pool, 0, 0, 0, slot_stride, 0, 0, _flat("slots", slots, B, torch.int32, dev), n, 0, 0, 0,
+                      _word("status", status, dev))
+        _check(_packed().vdn_linear_attn_step(a, b, c, o, cfg, _here(q)), "vdn_linear_attn_step")
     return out
 
 
-def _rows(name, t, shape, dtype, device):
-    """Pointer and row stride of a [rows, W] tensor."""
+def _rows(name, t, like, dtype):
+    """Pointer and row stride of a tensor of ``dtype`` with the [rows, W] shape and the device of ``like``; 0 for None."""
     if t is None:
-        return None, 0
-    _match(name, t, shape, dtype, device)
-    if shape[0] <= 1:
-        return t.data_ptr(), shape[1]
-    if t.stride(0) < shape[1]:
+        return 0, 0
+    if t.shape != like.shape or t.dtype != dtype or t.device != like.device:
+        raise ValueError(f"{name}: expected {tuple(like.shape)} {dtype} on {like.device}, got {tuple(t.shape)} {t.dtype} "
+                         f"on {t.device}")
+    (rows, W), (s0, s1) = t.shape, t.stride()
+    if s1 != 1 and W != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    if rows <= 1:
+        return t.data_ptr(), 0
+    if s0 < W:
         raise ValueError(f"{name}: rows must not overlap")
-    return t.data_ptr(), t.stride(0)
+    return t.data_ptr(), s0
 
 
-def _norm_cfg(x, weight, eps) -> VdnNormCfg:
+def _matrix(x):
     if x.dim() != 2 or x.dtype not in _DTYPES:
         raise ValueError(f"expected a [rows, width] bf16 or fp32 tensor, got {tuple(x.shape)} {x.dtype}")
+    return x.shape
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_bytes(rows, W, dtype):
     cfg = VdnNormCfg()
-    cfg.rows, cfg.width, cfg.dtype, cfg.eps = x.shape[0], x.shape[1], _DTYPES[x.dtype], eps
-    cfg.weight = _flat("weight", weight, x.shape[1], torch.float32, x.device)
-    return cfg
+    cfg.rows, cfg.width, cfg.dtype = rows, W, _DTYPES[dtype]
+    n = library().vdn_norm_workspace_bytes(ctypes.byref(cfg))
+    if n == 0:
+        _check(library().vdn_norm_validate(ctypes.byref(cfg)), "vdn_norm_workspace_bytes")
+    return n
 
 
 def add_rmsnorm_fwd(x, weight=None, *, residual=None, residual_out=None, eps: float = -1.0,
@@ -673,30 +710,31 @@ def add_rmsnorm_fwd(x, weight=None, *, residual=None, residual_out=None, eps: fl
     [rows, W] and fp32 scales [rows, 1] / [rows, ceil(W / 128)], y ~ value *
     scale."""
     with _on(x, stream):
-        cfg = _norm_cfg(x, weight, eps)
-        rows, W = x.shape
-        cfg.output = out_mode
-        if out_mode not in (NORM_OUT_TENSOR, NORM_OUT_E4M3_ROW, NORM_OUT_E4M3_GROUP):
-            raise VdnError(1, "vdn_add_rmsnorm_fwd")
-        quant = out_mode != NORM_OUT_TENSOR
-        kind = torch.float8_e4m3fn if quant else x.dtype
+        rows, W = _matrix(x)
+        dev = x.device
+        kind, ps = x.dtype, 0
+        if out_mode != NORM_OUT_TENSOR:
+            if out_mode not in (NORM_OUT_E4M3_ROW, NORM_OUT_E4M3_GROUP):
+                raise VdnError(1, "vdn_add_rmsnorm_fwd")
+            kind = torch.float8_e4m3fn
+            groups = 1 if out_mode == NORM_OUT_E4M3_ROW else (W + 127) // 128
+            if scales is None:
+                scales = torch.empty((rows, groups), dtype=torch.float32, device=dev)
+            elif scales.shape != (rows, groups) or scales.dtype != torch.float32 or scales.device != dev \
+                    or not scales.is_contiguous():
+                raise ValueError(f"scales: expected a contiguous {(rows, groups)} torch.float32 on {dev}, got "
+                                 f"{tuple(scales.shape)} {scales.dtype} on {scales.device}")
+            ps = scales.data_ptr()
         if out is None:
-            out = torch.empty((rows, W), dtype=kind, device=x.device)
-        groups = (1 if out_mode == NORM_OUT_E4M3_ROW else (W + 127) // 128) if quant else 0
-        if quant and scales is None:
-            scales = torch.empty((rows, groups), dtype=torch.float32, device=x.device)
-        px, cfg.x_stride = _rows("x", x, (rows, W), x.dtype, x.device)
-        pr, cfg.residual_stride = _rows("residual", residual, (rows, W), x.dtype, x.device)
-        ps, cfg.residual_out_stride = _rows("residual_out", residual_out, (rows, W), x.dtype, x.device)
-        po, cfg.out_stride = _rows("out", out, (rows, W), kind, x.device)
-        if quant:
-            _match("scales", scales, (rows, groups), torch.float32, x.device)
-            if not scales.is_contiguous():
-                raise ValueError("scales: must be contiguous")
-        code = library().vdn_add_rmsnorm_fwd(px, pr, ps, po, _ptr(scales) if quant else None, ctypes.byref(cfg),
-                                             _stream())
-        _check(code, "vdn_add_rmsnorm_fwd")
-    return (out, scales) if quant else out
+            out = torch.empty(x.shape, dtype=kind, device=dev)
+        px, x_stride = _rows("x", x, x, x.dtype)
+        pr, r_stride = _rows("residual", residual, x, x.dtype)
+        ph, h_stride = _rows("residual_out", residual_out, x, x.dtype)
+        po, o_stride = _rows("out", out, x, kind)
+        cfg = _NORM(rows, W, _DTYPES[x.dtype], out_mode, eps, _flat("weight", weight, W, torch.float32, dev), x_stride,
+                    r_stride, h_stride, o_stride, 0, 0, 0, 0, 0)
+        _check(_packed().vdn_add_rmsnorm_fwd(px, pr, ph, po, ps, cfg, _here(x)), "vdn_add_rmsnorm_fwd")
+    return out if ps == 0 and kind is x.dtype else (out, scales)
 
 
 def add_rmsnorm_bwd(h, weight, dy, *, dh=None, eps: float = -1.0, dx=None, dweight=None, want_dweight: bool = True,
@@ -706,26 +744,24 @@ def add_rmsnorm_bwd(h, weight, dy, *, dh=None, eps: float = -1.0, dx=None, dweig
     (None unless ``want_dweight``).  h: the stored residual_out (or x); dh: the
     gradient that reaches h from elsewhere, or None."""
     with _on(h, stream):
-        cfg = _norm_cfg(h, weight, eps)
-        rows, W = h.shape
+        rows, W = _matrix(h)
+        dev = h.device
         if dx is None:
-            dx = torch.empty((rows, W), dtype=h.dtype, device=h.device)
+            dx = torch.empty(h.shape, dtype=h.dtype, device=dev)
+        pw = ws_ptr = ws_bytes = 0
         if not want_dweight:
             dweight = None
-        elif dweight is None:
-            dweight = torch.empty(W, dtype=torch.float32, device=h.device)
-        ph, cfg.x_stride = _rows("h", h, (rows, W), h.dtype, h.device)
-        pdy, cfg.dy_stride = _rows("dy", dy, (rows, W), h.dtype, h.device)
-        pdh, cfg.dh_stride = _rows("dh", dh, (rows, W), h.dtype, h.device)
-        pdx, cfg.dx_stride = _rows("dx", dx, (rows, W), h.dtype, h.device)
-        pdw = _flat("dweight", dweight, W, torch.float32, h.device)
-        if pdw is not None:
-            if workspace is None:
-                n = library().vdn_norm_workspace_bytes(ctypes.byref(cfg))
-                if n == 0:
-                    _check(library().vdn_norm_validate(ctypes.byref(cfg)), "vdn_norm_workspace_bytes")
-                workspace = torch.empty(n, dtype=torch.uint8, device=h.device)
-            cfg.workspace, cfg.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-        code = library().vdn_add_rmsnorm_bwd(ph, pdy, pdh, pdx, pdw, ctypes.byref(cfg), _stream())
-        _check(code, "vdn_add_rmsnorm_bwd")
+        else:
+            if dweight is None:
+                dweight = torch.empty(W, dtype=torch.float32, device=dev)
+            pw = _flat("dweight", dweight, W, torch.float32, dev)
+            ws = _scratch(workspace, _norm_bytes(rows, W, h.dtype), dev)
+            ws_ptr, ws_bytes = ws.data_ptr(), ws.nbytes
+        ph, h_stride = _rows("h", h, h, h.dtype)
+        pdy, dy_stride = _rows("dy", dy, h, h.dtype)
+        pdh, dh_stride = _rows("dh", dh, h, h.dtype)
+        pdx, dx_stride = _rows("dx", dx, h, h.dtype)
+        cfg = _NORM(rows, W, _DTYPES[h.dtype], 0, eps, _flat("weight", weight, W, torch.float32, dev), h_stride, 0, 0, 0,
+                    dy_stride, dh_stride, dx_stride, ws_ptr, ws_bytes)
+        _check(_packed().vdn_add_rmsnorm_bwd(ph, pdy, pdh, pdx, pw, cfg, _here(h)), "vdn_add_rmsnorm_bwd")
     return dx, dweight

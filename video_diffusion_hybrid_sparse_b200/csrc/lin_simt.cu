@@ -313,8 +313,8 @@ namespace {
 
 template <typename T, int D>
 cudaError_t states_simt(const LinStateParams& p, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(lin_states_simt<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       SimtLayout<D>::kBytes);
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = lin_prepare((const void*)lin_states_simt<T, D>, SimtLayout<D>::kBytes, 0, done);
   if (e != cudaSuccess) return e;
   lin_states_simt<T, D><<<dim3(p.pl.grid * p.pl.sub, p.n_walks), kThreads, SimtLayout<D>::kBytes, st>>>(p);
   return cudaGetLastError();
@@ -322,8 +322,8 @@ cudaError_t states_simt(const LinStateParams& p, cudaStream_t st) {
 
 template <typename T, int D>
 cudaError_t out_simt(const LinOutParams& p, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(lin_out_simt<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       SimtLayout<D>::kBytes);
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = lin_prepare((const void*)lin_out_simt<T, D>, SimtLayout<D>::kBytes, 0, done);
   if (e != cudaSuccess) return e;
   lin_out_simt<T, D><<<dim3(p.pl.grid, p.n_jobs), kThreads, SimtLayout<D>::kBytes, st>>>(p);
   return cudaGetLastError();

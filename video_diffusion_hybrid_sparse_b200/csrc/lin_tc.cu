@@ -937,12 +937,9 @@ namespace {
 
 template <int D>
 cudaError_t out_tc(const LinTcMaps& m, const LinOutParams& p, cudaStream_t st) {
+  static std::atomic<unsigned long long> done{0};
   // the warps' register shares are drawn from what the CTA was launched with
-  cudaFuncAttributes a;
-  cudaError_t e = cudaFuncGetAttributes(&a, lin_out_tc<D>);
-  if (e != cudaSuccess) return e;
-  if (a.numRegs < (int)kTcRegs) return cudaErrorInvalidConfiguration;
-  e = cudaFuncSetAttribute(lin_out_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, TcLayout<D>::kBytes);
+  const cudaError_t e = lin_prepare((const void*)lin_out_tc<D>, TcLayout<D>::kBytes, kTcRegs, done);
   if (e != cudaSuccess) return e;
   lin_out_tc<D><<<p.n_jobs * p.pl.grid, kTcThreads, TcLayout<D>::kBytes, st>>>(m, p);
   return cudaGetLastError();
@@ -950,13 +947,28 @@ cudaError_t out_tc(const LinTcMaps& m, const LinOutParams& p, cudaStream_t st) {
 
 template <int D>
 cudaError_t states_tc(const LinTcMaps& m, const LinStateParams& p, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(lin_states_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, StLayout<D>::kBytes);
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = lin_prepare((const void*)lin_states_tc<D>, StLayout<D>::kBytes, 0, done);
   if (e != cudaSuccess) return e;
   lin_states_tc<D><<<std::min(kLinSms, p.n_walks * p.pl.grid * p.pl.sub), kStThreads, StLayout<D>::kBytes, st>>>(m, p);
   return cudaGetLastError();
 }
 
 }  // namespace
+
+cudaError_t lin_prepare(const void* kernel, int smem_bytes, int min_regs, std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  cudaFuncAttributes a;
+  if ((e = cudaFuncGetAttributes(&a, kernel)) != cudaSuccess) return e;
+  if (a.numRegs < min_regs) return cudaErrorInvalidConfiguration;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 cudaError_t launch_lin_out_tc(const LinTcMaps& m, const LinOutParams& p, cudaStream_t st) {
   return p.d == 128 ? out_tc<128>(m, p, st) : out_tc<64>(m, p, st);

@@ -23,6 +23,8 @@
 // of R, so that the gradient by state_in is alpha times the last W.
 #pragma once
 
+#include <atomic>
+
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -144,6 +146,10 @@ struct LinStepParams {
   int n_slots;
   int* status;
 };
+
+// Sets a kernel's shared memory once on each device (the attribute belongs to the device's copy of the kernel) and checks
+// that it takes at least min_regs registers a thread there.
+cudaError_t lin_prepare(const void* kernel, int smem_bytes, int min_regs, std::atomic<unsigned long long>& done);
 
 // fp32: 1 for fp32 tensors, 0 for bf16
 cudaError_t launch_lin_states_simt(const LinStateParams& p, int D, int fp32, cudaStream_t st);
