@@ -33,7 +33,7 @@ struct NormBwdParams {
 // vec: rows and pointers are 16-byte aligned and W % 8 == 0
 cudaError_t launch_norm_fwd(const NormParams& p, int fp32, int output, int vec, cudaStream_t st);
 cudaError_t launch_norm_bwd(const NormBwdParams& p, int fp32, int vec, cudaStream_t st);
-// rows of partial weight gradients that launch_norm_bwd writes (also the count in NormBwdParams)
+// blocks of launch_norm_bwd, each of which leaves a partial weight gradient (also the count in NormBwdParams)
 int norm_parts(long long rows, int W);
 // bytes of launch_norm_bwd's parts (rows wider than registers: and two factors of each row)
 size_t norm_workspace(long long rows, int W);
