@@ -9,6 +9,7 @@
 // 128 and 64.  Bound by the FMA pipe: fp32 has no tensor-core form that keeps
 // fp32's products, which is what a caller of fp32 tensors asks for here.
 #include "lin_common.cuh"
+#include "pdl.cuh"
 
 namespace vdn {
 namespace {
@@ -105,6 +106,7 @@ __global__ void __launch_bounds__(kThreads) lin_states_simt(const __grid_constan
   float *Y = sm, *Z = Y + L::kTile, *W = Z + L::kTile, *w = W + D * D;
   const LinPlan& pl = p.pl;
   const LinWalk& wk = p.walk[blockIdx.y];
+  pdl_release();
   const int range = blockIdx.x / pl.sub;
   const int bh = (int)((pl.start(range + 1) - 1) / pl.nc), b = bh / p.H, h = bh % p.H, len = lin_length(p.lengths, b, p.N);
   const float l2 = lin_log2_decay(p.log_decay[h]);
@@ -137,6 +139,7 @@ __global__ void __launch_bounds__(kThreads) lin_out_simt(const __grid_constant__
   const int tid = threadIdx.x, rev = jb.reverse;
   long long t = pl.start(blockIdx.x);
   const long long t_end = pl.start(blockIdx.x + 1);
+  pdl_wait();
   while (t < t_end) {
     const LinPiece pc(t, t_end, pl);
     t += pc.u1 - pc.u0;
@@ -263,6 +266,7 @@ __global__ void __launch_bounds__(128) lin_scan(const __grid_constant__ LinState
   constexpr int kAhead = 8;
   const LinPlan& pl = p.pl;
   const LinWalk& wk = p.walk[blockIdx.y];
+  pdl_release();
   const int per = (DD + 4 * (int)blockDim.x - 1) / (4 * (int)blockDim.x);  // blocks of a head
   const int bh = blockIdx.x / per, b = bh / p.H, h = bh % p.H, sub = pl.sub;
   const long long head0 = (long long)bh * pl.nc;
@@ -282,6 +286,7 @@ __global__ void __launch_bounds__(128) lin_scan(const __grid_constant__ LinState
       fall[i / sub] = lin_pow(l2, lin_rows((int)(max(pl.start(j), head0) - head0), (int)(pl.start(j + 1) - head0), len, pl, wk.reverse));
   }
   __syncthreads();
+  pdl_wait();
   const int e = (blockIdx.x % per * blockDim.x + threadIdx.x) * 4;
   if (e >= DD) return;
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -325,6 +330,7 @@ cudaError_t out_simt(const LinOutParams& p, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
   const cudaError_t e = lin_prepare((const void*)lin_out_simt<T, D>, SimtLayout<D>::kBytes, 0, done);
   if (e != cudaSuccess) return e;
+  if (p.pl.split) return launch_after(lin_out_simt<T, D>, dim3(p.pl.grid, p.n_jobs), kThreads, SimtLayout<D>::kBytes, st, p);
   lin_out_simt<T, D><<<dim3(p.pl.grid, p.n_jobs), kThreads, SimtLayout<D>::kBytes, st>>>(p);
   return cudaGetLastError();
 }
@@ -344,8 +350,7 @@ cudaError_t launch_lin_out_simt(const LinOutParams& p, int D, int fp32, cudaStre
 }
 
 cudaError_t launch_lin_scan(const LinStateParams& p, int D, cudaStream_t st) {
-  lin_scan<<<dim3((D * D + 511) / 512 * p.B * p.H, p.n_walks), 128, 0, st>>>(p, D * D);
-  return cudaGetLastError();
+  return launch_after(lin_scan, dim3((D * D + 511) / 512 * p.B * p.H, p.n_walks), 128, 0, st, p, D * D);
 }
 
 }  // namespace vdn

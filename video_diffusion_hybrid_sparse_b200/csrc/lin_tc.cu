@@ -41,6 +41,7 @@
 #include <algorithm>
 
 #include "lin_common.cuh"
+#include "pdl.cuh"
 #include "sm100.cuh"
 #include "tma_encode.h"
 
@@ -113,10 +114,23 @@ struct WaitRecord {
 
 static_assert(kNumBars * 8 + 8 + sizeof(WaitRecord) <= 272, "barrier block");
 
+// A probe that may suspend the warp for a while: 26 warps that probe in a loop are shared-memory traffic.
+constexpr uint32_t kSuspendNs = 100000;
 // mbar_wait in few instructions (see the head of the file): the same bound in global time, read at every probe.
+__device__ __forceinline__ bool try_wait_long(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred P;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 P, [%1], %2, %3;\n\t"
+      "selp.b32 %0, 1, 0, P;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(kSuspendNs)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ bool lin_wait(uint64_t* bar, uint32_t parity, WaitRecord* rec, long long limit_ns = kWaitNs) {
   long long t0 = 0;
-  while (!mbar_try_wait(bar, parity)) {
+  while (!try_wait_long(bar, parity)) {
     if (*reinterpret_cast<volatile int*>(&rec->given_up)) return false;
     const long long t = global_ns();
     if (t0 == 0) {
@@ -578,7 +592,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lin_out_tc(const __grid_constan
       arrive_warp(&bars[kWReady]);
     };
     int c = 0;
-    bool ok = true;
+    bool ok = true, waited = false;  // for the scan: the other warps need the call's inputs only
     for (long long t = t_begin; t < t_end && ok;) {
       const LinPiece pc(t, t_end, pl);
       t += pc.u1 - pc.u0;
@@ -596,6 +610,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) lin_out_tc(const __grid_constan
           *reinterpret_cast<uint4*>(o + (long long)(row0 + r) * jb.o.sn + e) = make_uint4(0, 0, 0, 0);
       }
       // the state before the piece
+      if (!waited) pdl_wait();
+      waited = true;
       const float* src = nullptr;
       float mul = 1.f;
       if (pc.u0 > 0) {
@@ -773,6 +789,7 @@ __global__ void __launch_bounds__(kStThreads, 1) lin_states_tc(const __grid_cons
   WaitRecord* ab = reinterpret_cast<WaitRecord*>(smem + L::kBar + sNumBars * 8 + 8);
   const LinPlan& pl = p.pl;
   const int n_pieces = p.n_walks * pl.grid * pl.sub;
+  pdl_release();
   const uint32_t warp = warp_id(), lane = lane_id();
 
   if (threadIdx.x == 0) {
@@ -941,6 +958,7 @@ cudaError_t out_tc(const LinTcMaps& m, const LinOutParams& p, cudaStream_t st) {
   // the warps' register shares are drawn from what the CTA was launched with
   const cudaError_t e = lin_prepare((const void*)lin_out_tc<D>, TcLayout<D>::kBytes, kTcRegs, done);
   if (e != cudaSuccess) return e;
+  if (p.pl.split) return launch_after(lin_out_tc<D>, p.n_jobs * p.pl.grid, kTcThreads, TcLayout<D>::kBytes, st, m, p);
   lin_out_tc<D><<<p.n_jobs * p.pl.grid, kTcThreads, TcLayout<D>::kBytes, st>>>(m, p);
   return cudaGetLastError();
 }

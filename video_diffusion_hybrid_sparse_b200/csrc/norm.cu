@@ -18,6 +18,7 @@
 #include <type_traits>
 
 #include "norm.h"
+#include "pdl.cuh"
 #include "sm100.cuh"
 
 namespace vdn {
@@ -476,6 +477,7 @@ __global__ void __launch_bounds__(block_of(G), G <= 256 ? 2 : 1) norm_bwd(const 
   __shared__ float s_sq[32], s_gh[32];
   __shared__ uint64_t s_acc[kRows > 1 ? kRows - 1 : 1][kRows > 1 ? G * kV * kE / 2 : 1];
   const int t = threadIdx.x % G, group = threadIdx.x / G;
+  pdl_release();
   using C = Columns<G, kVec>;
   Pairs acc[kV];
 #pragma unroll
@@ -633,6 +635,7 @@ __global__ void __launch_bounds__(256) norm_dweight_wide(const __grid_constant__
 // dweight[col] = sum of the parts, in a fixed order
 __global__ void __launch_bounds__(1024) norm_dweight(const float* parts, int n_parts, int W, float* dweight) {
   __shared__ float s[32][33];
+  pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
   float a = 0.f;
   if (col < W)
@@ -722,8 +725,7 @@ cudaError_t bwd(const NormBwdParams& p, int vec, cudaStream_t st) {
     });
   }
   if (e != cudaSuccess || !p.parts) return e;
-  norm_dweight<<<(p.W + 31) / 32, 1024, 0, st>>>(p.parts, p.n_parts, p.W, p.dweight);
-  return cudaGetLastError();
+  return launch_after(norm_dweight, (p.W + 31) / 32, 1024, 0, st, (const float*)p.parts, p.n_parts, p.W, p.dweight);
 }
 
 }  // namespace
