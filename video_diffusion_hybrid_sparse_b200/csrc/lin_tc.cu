@@ -57,9 +57,9 @@ struct TcLayout {
   static constexpr int kLo = kSlots * kTile;                 // second and third part of 64 rows of the decayed Y
   static constexpr int kW = kLo + kTile;                     // bf16(W), [z box of 64][y][64]
   static constexpr int kZero = kW + D * D * 2;               // D = 64: the upper half of a 128-row A operand, one K step
-  static constexpr int kTab = kZero + (D == 64 ? 2048 : 0);  // lambda^0..31 of a piece's head, two tables in turn
+  static constexpr int kTab = kZero + (D == 64 ? 2048 : 0);  // lambda^0..31 of a piece's head between zeros, two in turn
   static constexpr int kStage = D == 128 ? kW : kTab + 1024;  // its rows on their way out: W's tile (see there), or 8 x 2 KB
-  static constexpr int kBar = D == 128 ? kTab + 2 * 128 : kStage + 8 * 2048;
+  static constexpr int kBar = D == 128 ? kTab + 2 * 384 : kStage + 8 * 2048;
   static constexpr int kBytes = kBar + 288 + 1024;
 };
 static_assert(TcLayout<128>::kBytes <= 232448 && TcLayout<64>::kBytes <= 232448, "shared memory of an SM");
@@ -481,8 +481,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) lin_out_tc(const __grid_constan
       const float l2 = lin_log2_decay(p.log_decay[h]);
       // Every warp writes the same table.  One that is ahead fills the other: it has passed a chunk of this piece, which
       // takes all warps, before it comes to the next but one.
-      float* pw = reinterpret_cast<float*>(smem + L::kTab) + (table ^= 32);
+      float* pw = reinterpret_cast<float*>(smem + L::kTab) + (table ^= 96) + 32;
       pw[lane] = lin_pow(l2, rev ? lane : 31 - lane);
+      pw[(int)lane - 32] = pw[lane + 32] = 0.f;
       __syncwarp();
       const bool final_piece = jb.final_out && pc.u1 == pl.nc;
       // decay of row i, column j of a block before the diagonal: near * pw[j], both powers non-negative
@@ -519,14 +520,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) lin_out_tc(const __grid_constan
                 out[e] = f32x2_to_bf16x2(f32x2_mul(f32x2_mul(v, near2), e & 1 ? f[e >> 1].y : f[e >> 1].x));
               }
             } else {
-              const int f0 = hb * 16 + (rev ? -(int)lane : 31 - (int)lane);  // place of the first column's power
+              // the row's powers lie from a place of its own on; masked scores go whatever they are
+              const float* f = pw + hb * 16 + (rev ? -(int)lane : 31 - (int)lane);
+              const uint32_t keep = (rev ? 0xFFFFFFFFu << lane : 0xFFFFFFFFu >> (31 - lane)) >> (hb * 16);
+              float w[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) w[e] = f[e];
               tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const int f = f0 + 2 * e, g = f + 1;
-                out[e] = pack_bf16x2((unsigned)f < 32u ? __uint_as_float(s[2 * e]) * pw[f & 31] : 0.f,
-                                     (unsigned)g < 32u ? __uint_as_float(s[2 * e + 1]) * pw[g & 31] : 0.f);
-              }
+              for (int e = 0; e < 16; ++e) w[e] = keep >> e & 1 ? __uint_as_float(s[e]) * w[e] : 0.f;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) out[e] = pack_bf16x2(w[2 * e], w[2 * e + 1]);
             }
             if (n < kChunk) {
               const int cols = q * 32 + (int)lane < n ? n - block * 32 - hb * 16 : 0;  // real columns
