@@ -163,6 +163,21 @@ __device__ __forceinline__ void report(const WaitRecord& w, int* status, int* r,
   r[kRecSm] = sm_id();
 }
 
+// A place in a ring of kSlots with the phase of its barriers.
+template <int kSlots>
+struct Ring {
+  int slot;
+  uint32_t phase;
+  __device__ __forceinline__ Ring(int at = 0) : slot(at), phase(0) {}
+  __device__ __forceinline__ void advance(int n) {
+    slot += n;
+    if (slot >= kSlots) {
+      slot -= kSlots;
+      phase ^= 1;
+    }
+  }
+};
+
 // One arrival for the warp, after what all its lanes did before (arrivals of 32 lanes are 32 turns of shared memory).
 __device__ __forceinline__ void arrive_warp(uint64_t* bar) {
   __syncwarp();
@@ -349,6 +364,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lin_out_tc(const __grid_constan
       // ------------------------------------------------------------ loads: X, Y, Z of each chunk
       int i = 0;
       bool ok = true;
+      Ring<L::kSlots> ring;
       const MapRef mx(maps.m[jb.mx]), my(maps.m[jb.my]), mz(maps.m[jb.mz]);
       for (long long t = t_begin; t < t_end && ok;) {
         const LinPiece pc(t, t_end, pl);
@@ -359,14 +375,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) lin_out_tc(const __grid_constan
         for (int u = ua; u < ub && ok; ++u) {
           const int row = (rev ? pl.nc - 1 - u : u) * kChunk;
 #pragma unroll
-          for (int k = 0; k < 3; ++k, ++i) {
-            const int s = i % L::kSlots;
+          for (int k = 0; k < 3; ++k, ++i, ring.advance(1)) {
             const MapRef& m = k == 0 ? mx : k == 1 ? my : mz;
-            if (!lin_wait(&bars[kEmpty + s], ((i / L::kSlots) & 1) ^ 1, ab)) {
+            if (!lin_wait(&bars[kEmpty + ring.slot], ring.phase ^ 1, ab)) {
               ok = false;
               break;
             }
-            load_tile<D>(smem + s * L::kTile, m, &bars[kFull + s], h, row, b);
+            load_tile<D>(smem + ring.slot * L::kTile, m, &bars[kFull + ring.slot], h, row, b);
           }
         }
       }
@@ -388,72 +403,75 @@ __global__ void __launch_bounds__(kTcThreads, 1) lin_out_tc(const __grid_constan
       }
       constexpr uint32_t id_s = idesc_bf16_f32(128, kChunk, 0, 0), id_o = idesc_bf16_f32(128, D, 0, 1);
       const uint32_t base = smem_u32(smem);
-      auto slot = [](int t) { return t % L::kSlots; };
-      auto tile = [&](int t) { return fresh(base) + slot(t) * L::kTile; };
+      using R = Ring<L::kSlots>;
+      R x(0), y(1), z(2);  // the chunk's tiles
+      auto tile = [&](const R& t) { return fresh(base) + t.slot * L::kTile; };
       auto wait = [&](uint64_t* bar, uint32_t ph, long long limit = kWaitNs) {
         const bool got = __all_sync(0xffffffffu, lin_wait(bar, ph, ab, limit));
         tc_fence_after();
         return got;
       };
-      auto loaded = [&](int t) { return wait(&bars[kFull + slot(t)], (t / L::kSlots) & 1); };
+      auto loaded = [&](const R& t) { return wait(&bars[kFull + t.slot], t.phase); };
       if (warp == 1) {
         // failure-path test: wait, with a short limit, for a phase that only this warp's own commit completes
         bool ok = !(p.inject_timeout && blockIdx.x == 0 && !wait(&bars[kSFull], 0, 10000000ll));
         for (int c = -1; c < total && ok; ++c) {
           const uint32_t ph = c & 1;
           if (c >= 0) {
-            if (!loaded(3 * c + 2) || !wait(&bars[kPReady], ph)) break;
+            if (!loaded(z) || !wait(&bars[kPReady], ph)) break;
             if (c > 0 && !wait(&bars[kOFree], ph ^ 1)) break;
             if (elect_one()) {
-              uint64_t dz = smem_desc(tile(3 * c + 2), kChunk * 128, 1024, kLayoutSw128);
+              uint64_t dz = smem_desc(tile(z), kChunk * 128, 1024, kLayoutSw128);
 #pragma unroll 1
               for (int kk = 0; kk < kChunk / 16; ++kk, dz += 128)
                 mma_ts(tmem + kColO1, tmem + kColS + (kk >> 1) * 32 + (kk & 1) * 8, dz, id_o, kk > 0);
               mma_commit(&bars[kOFull]);
-              mma_commit(&bars[kEmpty + slot(3 * c + 2)]);
+              mma_commit(&bars[kEmpty + z.slot]);
             }
             __syncwarp();
+            z.advance(3);
           }
           if (c + 1 == total) break;
-          const int t = 3 * (c + 1);
-          if (!loaded(t) || !loaded(t + 1)) break;
+          if (!loaded(x) || !loaded(y)) break;
           if (elect_one()) {
-            mma_columns<D, false>(tmem + kColS, tile(t), tile(t + 1), id_s);
+            mma_columns<D, false>(tmem + kColS, tile(x), tile(y), id_s);
             mma_commit(&bars[kSFull]);
-            mma_commit(&bars[kEmpty + slot(t)]);
-            mma_commit(&bars[kEmpty + slot(t + 1)]);
+            mma_commit(&bars[kEmpty + x.slot]);
+            mma_commit(&bars[kEmpty + y.slot]);
           }
           __syncwarp();
+          x.advance(3);
+          y.advance(3);
         }
       } else {
-        for (int c = 0; c < total; ++c) {
+        for (int c = 0; c < total; ++c, x.advance(3), y.advance(3), z.advance(3)) {
           const uint32_t ph = c & 1;
-          if (!loaded(3 * c) || !wait(&bars[kWReady], ph)) break;
+          if (!loaded(x) || !wait(&bars[kWReady], ph)) break;
           if (c > 0 && !wait(&bars[kOFree], ph ^ 1)) break;
           if (elect_one()) {
-            mma_columns<D, true>(tmem + kColO2, tile(3 * c), fresh(base) + L::kW, id_o);
+            mma_columns<D, true>(tmem + kColO2, tile(x), fresh(base) + L::kW, id_o);
             mma_commit(&bars[kOFull]);
-            mma_commit(&bars[kEmpty + slot(3 * c)]);
+            mma_commit(&bars[kEmpty + x.slot]);
           }
           __syncwarp();
-          const uint32_t y = tile(3 * c + 1), z = tile(3 * c + 2);
-          if (!loaded(3 * c + 2) || !wait(&bars[kYReady], ph)) break;
+          const uint32_t ty = tile(y), tz = tile(z);
+          if (!loaded(z) || !wait(&bars[kYReady], ph)) break;
           const int n_parts = parts_of[ph];  // as the decay warps have decided
           if (n_parts == 3) {
             if (elect_one()) {
-              mma_state<D>(tmem + kColDw, y, fresh(base) + L::kLo, fresh(base) + L::kZero, z, 0, 3);
+              mma_state<D>(tmem + kColDw, ty, fresh(base) + L::kLo, fresh(base) + L::kZero, tz, 0, 3);
               mma_commit(&bars[kYFree]);
             }
             __syncwarp();
           }
           if (!wait(&bars[kYReady2], ph)) break;
           if (elect_one()) {
-            if (n_parts == 2) mma_state<D>(tmem + kColDw, y, fresh(base) + L::kLo, fresh(base) + L::kZero, z, 0, 2);
-            mma_state<D>(tmem + kColDw, y + kHalf * 128, fresh(base) + L::kLo + (n_parts == 2 ? kHalf * D * 2 : 0),
-                         fresh(base) + L::kZero, z + kHalf * 128, 1, n_parts);
+            if (n_parts == 2) mma_state<D>(tmem + kColDw, ty, fresh(base) + L::kLo, fresh(base) + L::kZero, tz, 0, 2);
+            mma_state<D>(tmem + kColDw, ty + kHalf * 128, fresh(base) + L::kLo + (n_parts == 2 ? kHalf * D * 2 : 0),
+                         fresh(base) + L::kZero, tz + kHalf * 128, 1, n_parts);
             if (n_parts == 2) mma_commit(&bars[kYFree]);
-            mma_commit(&bars[kEmpty + slot(3 * c + 1)]);
-            mma_commit(&bars[kEmpty + slot(3 * c + 2)]);
+            mma_commit(&bars[kEmpty + y.slot]);
+            mma_commit(&bars[kEmpty + z.slot]);
             mma_commit(&bars[kDwFull]);
           }
           __syncwarp();
@@ -470,6 +488,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lin_out_tc(const __grid_constan
     const uint32_t s_lane = tmem_addr(tmem + kColS, q * 32, block * 32);
     const int away = rev ? block - q : q - block;  // blocks between P's columns and its rows' own; < 0: masked
     int c = 0, table = 0;
+    Ring<L::kSlots> ry(1), rz(2);
     bool ok = true;
     for (long long t = t_begin; t < t_end && ok;) {
       const LinPiece pc(t, t_end, pl);
@@ -488,15 +507,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) lin_out_tc(const __grid_constan
       const bool final_piece = jb.final_out && pc.u1 == pl.nc;
       // decay of row i, column j of a block before the diagonal: near * pw[j], both powers non-negative
       const float near = away > 0 ? lin_pow(l2, rev ? 32 * away - (int)lane : 32 * away - 31 + (int)lane) : 1.f;
-      for (int u = ua; u < ub; ++u, ++c) {
+      for (int u = ua; u < ub; ++u, ++c, ry.advance(3), rz.advance(3)) {
         const int row0 = (rev ? pl.nc - 1 - u : u) * kChunk, n = min(len - row0, kChunk);
         const uint32_t ph = c & 1;
-        const int ty = 3 * c + 1, tz = ty + 1;
-        uint8_t *y = smem + ty % L::kSlots * L::kTile, *parts = smem + L::kLo;
+        uint8_t *y = smem + ry.slot * L::kTile, *parts = smem + L::kLo;
         const bool third = final_piece && third_part(l2, lin_rows(u + 1, ub, len, pl, rev));
         if (tid == 0) parts_of[ph] = third ? 3 : 2;
         bool got = lin_wait(&bars[kSFull], ph, ab);
-        if (got && n < kChunk) got = lin_wait(&bars[kFull + tz % L::kSlots], (tz / L::kSlots) & 1, ab);
+        if (got && n < kChunk) got = lin_wait(&bars[kFull + rz.slot], rz.phase, ab);
         if (__any_sync(0xffffffffu, !got)) { ok = false; break; }
         tc_fence_after();
 #pragma unroll 1
@@ -542,7 +560,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lin_out_tc(const __grid_constan
           tmem_st8(s_lane + hb * 8, out);
         }
         if (n < kChunk) {
-          clear_rows<D, kDecay>(smem + tz % L::kSlots * L::kTile, tid, n);
+          clear_rows<D, kDecay>(smem + rz.slot * L::kTile, tid, n);
           fence_proxy_async_smem();
         }
         tmem_wait_st();
