@@ -184,6 +184,11 @@ __device__ __forceinline__ void arrive_warp(uint64_t* bar) {
   if (lane_id() == 0) mbar_arrive(bar);
 }
 
+// Weight of row r of a chunk with n real rows, `more` rows before the place it is decayed to.
+__device__ __forceinline__ float row_weight(float l2, int r, int n, int reverse, int more) {
+  return lin_pow(l2, more + (reverse ? r + 1 : max(n - 1 - r, 0)));
+}
+
 constexpr int kHalf = kChunk / 2;  // rows whose second and third parts are held at a time
 
 __device__ __forceinline__ uint64_t bf16x2_to_f32x2(uint32_t u) { return f32x2_pack(bf16_lo(u), bf16_hi(u)); }
@@ -193,28 +198,20 @@ __device__ __forceinline__ uint32_t f32x2_to_bf16x2(uint64_t v) {
   return pack_bf16x2(a, b);
 }
 
-// Decays rows row0 .. row0 + 63 of a tile of Y (128-byte rows, boxes of 64 columns): the first part in place, the second
-// and, if `third`, the third into `parts` (64 rows each, the same layout).  Rows from n on (padding, whatever it
-// holds) become zeros.  Weight of row r: lambda^(more + n - 1 - r) forward, lambda^(more + r + 1) in reverse.
-template <int D, int kThreads>
-__device__ __forceinline__ void decay_half(uint8_t* tile, uint8_t* parts, int row0, int tid, float l2, int n, int reverse,
-                                           int more, bool third) {
-  constexpr int kPart = kHalf * D * 2, kUnits = kPart / 16 / kThreads;
-  constexpr int kStep = kThreads / 8;                        // rows between a thread's 16-byte units
-  constexpr int kRows = kHalf > kStep ? kHalf / kStep : 1;  // different rows of a thread in a box
-  float w[kRows];
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    const int r = row0 + (tid / 8 + i * kStep) % kHalf;
-    w[i] = lin_pow(l2, more + (reverse ? r + 1 : max(n - 1 - r, 0)));
-  }
+// Decays rows row0 .. row0 + 63 of a tile of Y (128-byte rows, boxes of 64 columns) by 512 threads, of which each has one
+// row, w its weight: the first part in place, the second and, if `third`, the third into `parts` (64 rows each, the same
+// layout).  Rows from n on (padding, whatever it holds) become zeros.
+template <int D>
+__device__ __forceinline__ void decay_half(uint8_t* tile, uint8_t* parts, int row0, int tid, float w, int n, bool third) {
+  constexpr int kThreads = 512, kPart = kHalf * D * 2, kUnits = kPart / 16 / kThreads;
+  static_assert(kThreads / 8 == kHalf, "a thread's units lie in one row");
+  const uint64_t w2 = f32x2_pack(w, w);
 #pragma unroll
   for (int i = 0; i < kUnits; ++i) {
     const int off = (tid + i * kThreads) * 16;                                              // in a part
     uint8_t* y = tile + off / (kHalf * 128) * (kChunk * 128) + row0 * 128 + off % (kHalf * 128);  // in the tile
     uint4 v = *reinterpret_cast<const uint4*>(y);
-    if (row0 + off / 128 % kHalf >= n) v = make_uint4(0, 0, 0, 0);
-    const uint64_t w2 = f32x2_pack(w[i % kRows], w[i % kRows]);
+    if (row0 + tid / 8 >= n) v = make_uint4(0, 0, 0, 0);
     const uint32_t x[4] = {v.x, v.y, v.z, v.w};
     uint32_t u[4];
     uint64_t f[4];
@@ -505,6 +502,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) lin_out_tc(const __grid_constan
       pw[(int)lane - 32] = pw[lane + 32] = 0.f;
       __syncwarp();
       const bool final_piece = jb.final_out && pc.u1 == pl.nc;
+      // of this thread's rows of Y in a whole chunk
+      const float whole0 = row_weight(l2, tid / 8, kChunk, rev, 0), whole1 = row_weight(l2, kHalf + tid / 8, kChunk, rev, 0);
       // decay of row i, column j of a block before the diagonal: near * pw[j], both powers non-negative
       const float near = away > 0 ? lin_pow(l2, rev ? 32 * away - (int)lane : 32 * away - 31 + (int)lane) : 1.f;
       for (int u = ua; u < ub; ++u, ++c, ry.advance(3), rz.advance(3)) {
@@ -571,7 +570,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) lin_out_tc(const __grid_constan
 #pragma unroll 1
         for (int a = 0; a < 2; ++a) {
           if (a == 1 && third && __any_sync(0xffffffffu, !lin_wait(&bars[kYFree], ph, ab))) { ok = false; break; }
-          decay_half<D, kDecay>(y, parts + (third ? 0 : a * kHalf * D * 2), a * kHalf, tid, l2, n, rev, 0, third);
+          const float w = n == kChunk ? (a ? whole1 : whole0) : row_weight(l2, a * kHalf + tid / 8, n, rev, 0);
+          decay_half<D>(y, parts + (third ? 0 : a * kHalf * D * 2), a * kHalf, tid, w, n, third);
           fence_proxy_async_smem();
           arrive_warp(&bars[a ? kYReady2 : kYReady]);
         }
@@ -661,13 +661,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) lin_out_tc(const __grid_constan
           }
         }
       }
+      const float f_whole = alpha * lin_pow(l2, rev ? kChunk - 1 - r : r + 1), g_whole = lin_pow(l2, kChunk);
       if (ua < ub) publish();
       for (int u = ua; u < ub; ++u, ++c) {
         const int row0 = (rev ? pl.nc - 1 - u : u) * kChunk, n = min(len - row0, kChunk);
         const uint32_t ph = c & 1;
         if (__any_sync(0xffffffffu, !lin_wait(&bars[kOFull], ph, ab))) { ok = false; break; }
         tc_fence_after();
-        const float f = alpha * lin_pow(l2, rev ? max(n - 1 - r, 0) : r + 1);
+        const float f = n == kChunk ? f_whole : alpha * lin_pow(l2, rev ? max(n - 1 - r, 0) : r + 1);
         const uint64_t f2 = f32x2_pack(f, f), a2 = f32x2_pack(alpha, alpha);
         if (D == 64) staged();
 #pragma unroll 1
@@ -705,7 +706,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lin_out_tc(const __grid_constan
           tma_store_4d(om.map, stage, z0, h * (int)om.mh, row0 + q * 32, b * (int)om.mb);
         if (__any_sync(0xffffffffu, !lin_wait(&bars[kDwFull], ph, ab))) { ok = false; break; }
         tc_fence_after();
-        const float g = lin_pow(l2, n);
+        const float g = n == kChunk ? g_whole : lin_pow(l2, n);
         const uint64_t g2 = f32x2_pack(g, g);
         if (q * 32 < D) {
 #pragma unroll
@@ -928,8 +929,8 @@ __global__ void __launch_bounds__(kStThreads, 1) lin_states_tc(const __grid_cons
         if (n < kChunk) clear_rows<D, kStWorkers>(smem + tz % L::kSlots * L::kTile, tid, n);
 #pragma unroll 1
         for (int a = 0; a < 2; ++a)
-          decay_half<D, kStWorkers>(smem + ty % L::kSlots * L::kTile, smem + L::parts(c, a, third), a * kHalf, tid, pc.l2, n,
-                                    pc.rev, more, third);
+          decay_half<D>(smem + ty % L::kSlots * L::kTile, smem + L::parts(c, a, third), a * kHalf, tid,
+                        row_weight(pc.l2, a * kHalf + tid / 8, n, pc.rev, more), n, third);
         fence_proxy_async_smem();
         arrive_warp(&bars[sReady + (c & 1)]);
       }
