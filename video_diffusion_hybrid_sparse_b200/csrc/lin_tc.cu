@@ -247,20 +247,12 @@ __device__ __forceinline__ void clear_rows(uint8_t* z, int tid, int n) {
 // first row on
 template <int D, bool kBMn>
 __device__ __forceinline__ void mma_columns(uint32_t acc, uint32_t a, uint32_t b, uint32_t idesc) {
-  uint64_t da = smem_desc(a, 16, 1024, kLayoutSw128);
-  uint64_t db = kBMn ? smem_desc(b, D * 128, 1024, kLayoutSw128) : smem_desc(b, 16, 1024, kLayoutSw128);
-  uint32_t go = 0;
-#pragma unroll 1
-  for (int bx = 0; bx < D / 64; ++bx) {
-#pragma unroll 1
-    for (int kk = 0; kk < 4; ++kk) {
-      mma_ss(acc, da, db, idesc, go);
-      da += 2;
-      db += kBMn ? 128 : 2;
-      go = 1;
-    }
-    da += kChunk * 8 - 8;
-    if (!kBMn) db += kChunk * 8 - 8;
+  const uint64_t da = smem_desc(a, 16, 1024, kLayoutSw128);
+  const uint64_t db = kBMn ? smem_desc(b, D * 128, 1024, kLayoutSw128) : smem_desc(b, 16, 1024, kLayoutSw128);
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk) {
+    const uint64_t step = (kk >> 2) * (kChunk * 8) + (kk & 3) * 2;
+    mma_ss(acc, da + step, db + (kBMn ? (uint64_t)kk * 128 : step), idesc, kk > 0);
   }
 }
 
@@ -272,19 +264,13 @@ __device__ __forceinline__ void mma_state(uint32_t acc, uint32_t y, uint32_t par
   constexpr uint32_t idesc = idesc_bf16_f32(128, D, 1, 1);
   constexpr uint64_t step = D == 64 ? 128ull - (128ull << 16) : 128ull;
   const uint64_t dz = smem_desc(z, kChunk * 128, 1024, kLayoutSw128);
-  uint32_t a = y, lbo = kChunk * 128;
-#pragma unroll 1
-  for (int k = 0; k < n_parts; ++k) {
-    uint64_t da = smem_desc(a, D == 64 ? zero - a : lbo, 1024, kLayoutSw128), db = dz;
-#pragma unroll 1
-    for (int kk = 0; kk < kHalf / 16; ++kk) {
-      mma_ss(acc, da, db, idesc, go);
-      da += step;
-      db += 128;
-      go = 1;
-    }
-    a = parts + k * (kHalf * D * 2);
-    lbo = kHalf * 128;
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    if (k == 2 && n_parts < 3) break;
+    const uint32_t a = k == 0 ? y : parts + (k - 1) * (kHalf * D * 2);
+    const uint64_t da = smem_desc(a, D == 64 ? zero - a : k == 0 ? kChunk * 128 : kHalf * 128, 1024, kLayoutSw128);
+#pragma unroll
+    for (int kk = 0; kk < kHalf / 16; ++kk) mma_ss(acc, da + kk * step, dz + kk * 128, idesc, k || kk || go);
   }
 }
 
@@ -402,7 +388,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lin_out_tc(const __grid_constan
       const uint32_t base = smem_u32(smem);
       using R = Ring<L::kSlots>;
       R x(0), y(1), z(2);  // the chunk's tiles
-      auto tile = [&](const R& t) { return fresh(base) + t.slot * L::kTile; };
+      auto tile = [&](const R& t) { return base + t.slot * L::kTile; };
       auto wait = [&](uint64_t* bar, uint32_t ph, long long limit = kWaitNs) {
         const bool got = __all_sync(0xffffffffu, lin_wait(bar, ph, ab, limit));
         tc_fence_after();
@@ -418,10 +404,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) lin_out_tc(const __grid_constan
             if (!loaded(z) || !wait(&bars[kPReady], ph)) break;
             if (c > 0 && !wait(&bars[kOFree], ph ^ 1)) break;
             if (elect_one()) {
-              uint64_t dz = smem_desc(tile(z), kChunk * 128, 1024, kLayoutSw128);
-#pragma unroll 1
-              for (int kk = 0; kk < kChunk / 16; ++kk, dz += 128)
-                mma_ts(tmem + kColO1, tmem + kColS + (kk >> 1) * 32 + (kk & 1) * 8, dz, id_o, kk > 0);
+              const uint64_t dz = smem_desc(tile(z), kChunk * 128, 1024, kLayoutSw128);
+#pragma unroll
+              for (int kk = 0; kk < kChunk / 16; ++kk)
+                mma_ts(tmem + kColO1, tmem + kColS + (kk >> 1) * 32 + (kk & 1) * 8, dz + kk * 128, id_o, kk > 0);
               mma_commit(&bars[kOFull]);
               mma_commit(&bars[kEmpty + z.slot]);
             }
@@ -446,7 +432,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lin_out_tc(const __grid_constan
           if (!loaded(x) || !wait(&bars[kWReady], ph)) break;
           if (c > 0 && !wait(&bars[kOFree], ph ^ 1)) break;
           if (elect_one()) {
-            mma_columns<D, true>(tmem + kColO2, tile(x), fresh(base) + L::kW, id_o);
+            mma_columns<D, true>(tmem + kColO2, tile(x), base + L::kW, id_o);
             mma_commit(&bars[kOFull]);
             mma_commit(&bars[kEmpty + x.slot]);
           }
@@ -456,16 +442,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) lin_out_tc(const __grid_constan
           const int n_parts = parts_of[ph];  // as the decay warps have decided
           if (n_parts == 3) {
             if (elect_one()) {
-              mma_state<D>(tmem + kColDw, ty, fresh(base) + L::kLo, fresh(base) + L::kZero, tz, 0, 3);
+              mma_state<D>(tmem + kColDw, ty, base + L::kLo, base + L::kZero, tz, 0, 3);
               mma_commit(&bars[kYFree]);
             }
             __syncwarp();
           }
           if (!wait(&bars[kYReady2], ph)) break;
           if (elect_one()) {
-            if (n_parts == 2) mma_state<D>(tmem + kColDw, ty, fresh(base) + L::kLo, fresh(base) + L::kZero, tz, 0, 2);
-            mma_state<D>(tmem + kColDw, ty + kHalf * 128, fresh(base) + L::kLo + (n_parts == 2 ? kHalf * D * 2 : 0),
-                         fresh(base) + L::kZero, tz + kHalf * 128, 1, n_parts);
+            if (n_parts == 2) mma_state<D>(tmem + kColDw, ty, base + L::kLo, base + L::kZero, tz, 0, 2);
+            mma_state<D>(tmem + kColDw, ty + kHalf * 128, base + L::kLo + (n_parts == 2 ? kHalf * D * 2 : 0),
+                         base + L::kZero, tz + kHalf * 128, 1, n_parts);
             if (n_parts == 2) mma_commit(&bars[kYFree]);
             mma_commit(&bars[kEmpty + y.slot]);
             mma_commit(&bars[kEmpty + z.slot]);
@@ -888,11 +874,11 @@ __global__ void __launch_bounds__(kStThreads, 1) lin_states_tc(const __grid_cons
         const int n_parts = third_part(pc.l2, lin_rows(u + 1, pc.end, pc.len, pl, pc.rev)) ? 3 : 2;
         if (!(ok = wait(&bars[sFull + tz % L::kSlots], (tz / L::kSlots) & 1))) break;
         if (!(ok = wait(&bars[sReady + (c & 1)], (c >> 1) & 1))) break;
-        const uint32_t y = fresh(base) + ty % L::kSlots * L::kTile, z = fresh(base) + tz % L::kSlots * L::kTile;
+        const uint32_t y = base + ty % L::kSlots * L::kTile, z = base + tz % L::kSlots * L::kTile;
         if (elect_one()) {
 #pragma unroll 1
           for (int a = 0; a < 2; ++a)
-            mma_state<D>(acc, y + a * kHalf * 128, fresh(base) + L::parts(c, a, n_parts == 3), fresh(base) + L::kZero,
+            mma_state<D>(acc, y + a * kHalf * 128, base + L::parts(c, a, n_parts == 3), base + L::kZero,
                          z + a * kHalf * 128, u > pc.u0 || a > 0, n_parts);
           mma_commit(&bars[sEmpty + ty % L::kSlots]);
           mma_commit(&bars[sEmpty + tz % L::kSlots]);
