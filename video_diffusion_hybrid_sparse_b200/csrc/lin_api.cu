@@ -93,7 +93,7 @@ LinPlan make_plan(const vdn_linear_cfg* c, int jobs, int walks, bool tc) {
   pl.nc = std::max(1, (c->tokens + pl.chunk - 1) / pl.chunk);
   const long long heads = (long long)c->batch * c->heads;
   pl.total = heads * pl.nc;
-  const int per_wave = kLinSms * (tc ? 1 : 2);
+  const int per_wave = tc ? kLinSms : lin_simt_ctas(c->head_dim);
   const long long whole = (heads * jobs + per_wave - 1) / per_wave * pl.nc;
   const long long parts = (pl.total * (2 * jobs + walks) + 2 * per_wave - 1) / (2 * per_wave) + 8;
   pl.split = parts < whole;

@@ -1,13 +1,17 @@
-// lin_simt.cu - the causal linear memory on the FMA pipes: fp32 tensors, and
-// bf16 tensors of head_dim 32.
+// lin_simt.cu - the causal linear memory on the FMA pipes: fp32 tensors (and
+// bf16 tensors without a TMA view).
 //
-// A CTA walks its range of 32-row chunks with the state W (D x D, fp32) in
-// shared memory.  Per chunk: X, Y, Z rows (converted to fp32) are staged, the
-// scores X Y^T are formed, decayed and masked, then out = scores Z + X W and
-// W = lambda^n W + (decayed Y)^T Z.  32 rows keep the quadratic part (2 * 32 * D
-// multiply-adds a row) at a quarter to a half of the state's (2 * D * D) for D =
-// 128 and 64.  Bound by the FMA pipe: fp32 has no tensor-core form that keeps
-// fp32's products, which is what a caller of fp32 tensors asks for here.
+// A CTA walks its range of 64-row chunks with the state W (D x D, fp32) in
+// shared memory.  Per chunk: X, Y, Z rows (as fp32) are staged, the scores X Y^T
+// are formed, decayed and masked, then out = scores Z + X W and W = lambda^n W +
+// (decayed Y)^T Z.  fp32 has no tensor-core form that keeps fp32's products,
+// which is what a caller of fp32 tensors asks for, so the kernel is bound by the
+// FMA pipe, at 2 D (2 D + 64 + 32) operations a row: 64 rows keep the quadratic
+// part at a quarter (D = 128) to a half (64) of it, with the masked blocks of 16
+// columns and rows behind left out.  To be bound by it, a thread's tile has to
+// turn each load from shared memory into eight operations and more: 8 x 8 of the
+// state and 8 x 4 of the output at D = 128.  fp32 rows come by cp.async, the next
+// chunk's X while the state is updated.
 #include "lin_common.cuh"
 #include "pdl.cuh"
 
@@ -21,25 +25,30 @@ template <int D>
 struct SimtLayout {
   static constexpr int kPitch = D + 4;  // X, Y, Z rows: float4 reads of 8 rows at once meet no bank twice
   static constexpr int kTile = kC * kPitch;
-  static constexpr int kPP = kC + 1;
+  static constexpr int kPP = kC + 4;
   static constexpr int kFloats = 3 * kTile + D * D + kC * kPP + 2 * kC + 4;
   static constexpr int kBytes = kFloats * 4;
+  static constexpr int kCtas = D == 128 ? 1 : 2;  // on an SM: shared memory at D = 128, registers
 };
 
-// rows [row0, row0 + kC) of a view's (b, h) as fp32 into dst, zeros from n_valid on
+// rows [row0, row0 + kC) of a view's (b, h) as fp32 into dst, zeros from n_valid on; fp32 rows are on their way on return
 template <typename T, int D>
 __device__ __forceinline__ void load_rows(float* dst, const LinView& v, int b, int h, int row0, int n_valid) {
   constexpr int kVec = 16 / sizeof(T);
   constexpr int kPerRow = D / kVec;
   const T* base = static_cast<const T*>(v.p) + b * v.sb + h * v.sh;
+#pragma unroll 4
   for (int i = threadIdx.x; i < kC * kPerRow; i += kThreads) {
     const int r = i / kPerRow, c = (i - r * kPerRow) * kVec;
     float* d = dst + r * SimtLayout<D>::kPitch + c;
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (r < n_valid) w = *reinterpret_cast<const uint4*>(base + (long long)(row0 + r) * v.sn + c);
+    const T* src = base + (long long)(row0 + (r < n_valid ? r : 0)) * v.sn + c;
     if constexpr (sizeof(T) == 4) {
-      *reinterpret_cast<uint4*>(d) = w;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(d)), "l"(src),
+                   "r"(r < n_valid ? 16 : 0)
+                   : "memory");
     } else {
+      uint4 w = make_uint4(0, 0, 0, 0);
+      if (r < n_valid) w = *reinterpret_cast<const uint4*>(src);
       const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -48,6 +57,10 @@ __device__ __forceinline__ void load_rows(float* dst, const LinView& v, int b, i
       }
     }
   }
+}
+__device__ __forceinline__ void rows_arrived() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
 }
 
 __device__ __forceinline__ void store4(float* p, const float (&v)[4]) {
@@ -58,36 +71,50 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&v)[4]) {
   *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
 }
 
-// W = decay W + sum_r w[r] Y[r]^T Z[r] over the n real rows
+// A thread's tile of the state: kT x kT elements, in runs of four (two at D = 32) 64 apart, so that the runs of a warp's
+// threads are neighbours.
 template <int D>
-__device__ __forceinline__ void update_state(float* W, const float* Y, const float* Z, const float* w, float decay, int n) {
-  constexpr int kT = D / 16;
-  constexpr int kPitch = SimtLayout<D>::kPitch;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float acc[kT][kT];
+struct StateTile {
+  static constexpr int kT = D / 16, kRun = kT < 4 ? kT : 4, kRuns = kT / kRun;
+  float a[kT][kT];
+  __device__ __forceinline__ static int at(int thread, int i) { return thread * kRun + i / kRun * 64 + i % kRun; }
+  __device__ __forceinline__ static void load(float (&f)[kT], const float* p, int thread) {
 #pragma unroll
-  for (int i = 0; i < kT; ++i)
-#pragma unroll
-    for (int j = 0; j < kT; ++j) acc[i][j] = 0.f;
-  for (int r = 0; r < n; ++r) {
-    float y[kT], z[kT];
-#pragma unroll
-    for (int i = 0; i < kT; ++i) y[i] = w[r] * Y[r * kPitch + ty + 16 * i];
-#pragma unroll
-    for (int j = 0; j < kT; ++j) z[j] = Z[r * kPitch + tx + 16 * j];
+    for (int k = 0; k < kRuns; ++k) {
+      if constexpr (kRun == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(p + thread * 4 + 64 * k);
+        f[4 * k] = v.x, f[4 * k + 1] = v.y, f[4 * k + 2] = v.z, f[4 * k + 3] = v.w;
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(p + thread * 2);
+        f[0] = v.x, f[1] = v.y;
+      }
+    }
+  }
+  __device__ __forceinline__ void zero() {
 #pragma unroll
     for (int i = 0; i < kT; ++i)
 #pragma unroll
-      for (int j = 0; j < kT; ++j) acc[i][j] = fmaf(y[i], z[j], acc[i][j]);
+      for (int j = 0; j < kT; ++j) a[i][j] = 0.f;
   }
+  // a += sum_r w[r] Y[r]^T Z[r] over n rows
+  __device__ __forceinline__ void add(const float* Y, const float* Z, const float* w, int n) {
+    constexpr int kPitch = SimtLayout<D>::kPitch;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll 4
+    for (int r = 0; r < n; ++r) {
+      float y[kT], z[kT];
+      load(y, Y + r * kPitch, ty);
+      load(z, Z + r * kPitch, tx);
+      const float f = w[r];
 #pragma unroll
-  for (int i = 0; i < kT; ++i)
+      for (int i = 0; i < kT; ++i) y[i] *= f;
 #pragma unroll
-    for (int j = 0; j < kT; ++j) {
-      float* p = W + (ty + 16 * i) * D + tx + 16 * j;
-      *p = fmaf(decay, *p, acc[i][j]);
+      for (int i = 0; i < kT; ++i)
+#pragma unroll
+        for (int j = 0; j < kT; ++j) a[i][j] = fmaf(y[i], z[j], a[i][j]);
     }
-}
+  }
+};
 
 // weights lambda^(n - p - e) of the rows of a chunk (p: place in walk order)
 __device__ __forceinline__ void row_weights(float* w, float l2, int n, int reverse) {
@@ -97,13 +124,73 @@ __device__ __forceinline__ void row_weights(float* w, float l2, int n, int rever
   }
 }
 
+// P = scores, decayed by the rows between and 0 past the row in walk order: 4 x 4 a thread, rows and columns 16 apart, so
+// that whole blocks of 16 x 16 fall to the mask and are left out.
+template <int D, bool kRev>
+__device__ __forceinline__ void scores(float* P, const float* X, const float* Y, const float* pw, int n) {
+  using L = SimtLayout<D>;
+  const int c0 = threadIdx.x & 15, r0 = threadIdx.x >> 4;
+  float acc[4][4] = {};
+#pragma unroll 2
+  for (int k = 0; k < D; k += 4) {
+    float4 x[4], y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = *reinterpret_cast<const float4*>(X + (r0 + 16 * i) * L::kPitch + k);
+      y[i] = *reinterpret_cast<const float4*>(Y + (c0 + 16 * i) * L::kPitch + k);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (kRev ? j < i : j > i) continue;
+        acc[i][j] = fmaf(x[i].x, y[j].x, acc[i][j]);
+        acc[i][j] = fmaf(x[i].y, y[j].y, acc[i][j]);
+        acc[i][j] = fmaf(x[i].z, y[j].z, acc[i][j]);
+        acc[i][j] = fmaf(x[i].w, y[j].w, acc[i][j]);
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int r = r0 + 16 * i, c = c0 + 16 * j, gap = kRev ? c - r : r - c;
+      P[r * L::kPP + c] = gap >= 0 && r < n && c < n ? acc[i][j] * pw[gap] : 0.f;
+    }
+}
+
+// o[i] += sum_k A[row i][k] B[k][4 columns], k0 <= k < k1 (multiples of 4); A's rows are the same for a warp's neighbours
+template <int kR>
+__device__ __forceinline__ void rows_times(float (&o)[kR][4], const float* A, int a_pitch, const float* B, int b_pitch, int k0,
+                                           int k1) {
+#pragma unroll 2
+  for (int k = k0; k < k1; k += 4) {
+    float4 a[kR];
+#pragma unroll
+    for (int i = 0; i < kR; ++i) a[i] = *reinterpret_cast<const float4*>(A + i * a_pitch + k);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float4 v = *reinterpret_cast<const float4*>(B + (k + e) * b_pitch);
+#pragma unroll
+      for (int i = 0; i < kR; ++i) {
+        const float f = e == 0 ? a[i].x : e == 1 ? a[i].y : e == 2 ? a[i].z : a[i].w;
+        o[i][0] = fmaf(f, v.x, o[i][0]);
+        o[i][1] = fmaf(f, v.y, o[i][1]);
+        o[i][2] = fmaf(f, v.z, o[i][2]);
+        o[i][3] = fmaf(f, v.w, o[i][3]);
+      }
+    }
+  }
+}
+
 }  // namespace
 
+// A range's part, in pieces (linear.h); the state stays in registers.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) lin_states_simt(const __grid_constant__ LinStateParams p) {
   using L = SimtLayout<D>;
   extern __shared__ float sm[];
-  float *Y = sm, *Z = Y + L::kTile, *W = Z + L::kTile, *w = W + D * D;
+  float *Y = sm, *Z = Y + L::kTile, *w = Z + L::kTile;
   const LinPlan& pl = p.pl;
   const LinWalk& wk = p.walk[blockIdx.y];
   pdl_release();
@@ -112,20 +199,28 @@ __global__ void __launch_bounds__(kThreads) lin_states_simt(const __grid_constan
   const float l2 = lin_log2_decay(p.log_decay[h]);
   const LinStretch st = lin_piece_of(lin_stretch(range, len, l2, pl, wk.reverse), blockIdx.x % pl.sub, pl);
   if (st.u0 == st.u1) return;
-  for (int i = threadIdx.x; i < D * D; i += kThreads) W[i] = 0.f;
+  StateTile<D> W;
+  W.zero();
   for (int u = st.u0; u < st.u1; ++u) {
     const int row0 = (wk.reverse ? pl.nc - 1 - u : u) * kC, n = min(max(len - row0, 0), kC);
     __syncthreads();
     load_rows<T, D>(Y, wk.y, b, h, row0, n);
     load_rows<T, D>(Z, wk.z, b, h, row0, n);
     row_weights(w, l2, n, wk.reverse);
-    __syncthreads();
-    update_state<D>(W, Y, Z, w, lin_pow(l2, n), n);
+    const float fall = lin_pow(l2, n);
+#pragma unroll
+    for (int i = 0; i < W.kT; ++i)
+#pragma unroll
+      for (int j = 0; j < W.kT; ++j) W.a[i][j] *= fall;
+    rows_arrived();
+    W.add(Y, Z, w, n);
   }
-  __syncthreads();
   const float left = lin_pow(l2, lin_rows(st.u1, st.end, len, pl, wk.reverse));  // decay to the stretch's end
   float* dst = wk.parts + (long long)blockIdx.x * D * D;
-  for (int i = threadIdx.x; i < D * D; i += kThreads) dst[i] = left * W[i];
+#pragma unroll
+  for (int i = 0; i < W.kT; ++i)
+#pragma unroll
+    for (int j = 0; j < W.kT; ++j) dst[W.at(threadIdx.x >> 4, i) * D + W.at(threadIdx.x & 15, j)] = left * W.a[i][j];
 }
 
 template <typename T, int D>
@@ -137,6 +232,9 @@ __global__ void __launch_bounds__(kThreads) lin_out_simt(const __grid_constant__
   const LinPlan& pl = p.pl;
   const LinJob& jb = p.job[blockIdx.y];
   const int tid = threadIdx.x, rev = jb.reverse;
+  // output tile of a thread: kR rows of four columns
+  constexpr int kQuads = D / 4, kR = kC / (kThreads / kQuads);
+  const int c = tid % kQuads * 4, r0 = tid / kQuads * kR;
   long long t = pl.start(blockIdx.x);
   const long long t_end = pl.start(blockIdx.x + 1);
   pdl_wait();
@@ -159,98 +257,73 @@ __global__ void __launch_bounds__(kThreads) lin_out_simt(const __grid_constant__
     }
     for (int i = tid; i < D * D; i += kThreads)
       W[i] = src ? mul * (jb.transposed ? src[(i % D) * D + i / D] : src[i]) : 0.f;
+    auto first_row = [&](int u) { return (rev ? pl.nc - 1 - u : u) * kC; };
+    auto rows_of = [&](int u) { return min(max(len - first_row(u), 0), kC); };
+    load_rows<T, D>(X, jb.x, b, h, first_row(pc.u0), rows_of(pc.u0));
+    load_rows<T, D>(Y, jb.y, b, h, first_row(pc.u0), rows_of(pc.u0));
+    load_rows<T, D>(Z, jb.z, b, h, first_row(pc.u0), rows_of(pc.u0));
     for (int u = pc.u0; u < pc.u1; ++u) {
-      const int row0 = (rev ? pl.nc - 1 - u : u) * kC;
-      const int n_rows = min(p.N - row0, kC), n = min(max(len - row0, 0), kC);
-      __syncthreads();
-      load_rows<T, D>(X, jb.x, b, h, row0, n);
-      load_rows<T, D>(Y, jb.y, b, h, row0, n);
-      load_rows<T, D>(Z, jb.z, b, h, row0, n);
+      const int row0 = first_row(u), n_rows = min(p.N - row0, kC), n = rows_of(u);
       row_weights(w, l2, n, rev);
-      __syncthreads();
-      // scores: row r, columns c and c + 16, decayed by the rows between, 0 past the row in walk order
-      {
-        const int c0 = tid & 15, r0 = tid >> 4;
-        float acc[2][2] = {};
-        for (int k = 0; k < D; k += 4) {
-          float4 x[2], y[2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            x[i] = *reinterpret_cast<const float4*>(X + (r0 + 16 * i) * L::kPitch + k);
-            y[i] = *reinterpret_cast<const float4*>(Y + (c0 + 16 * i) * L::kPitch + k);
-          }
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              acc[i][j] = fmaf(x[i].x, y[j].x, acc[i][j]);
-              acc[i][j] = fmaf(x[i].y, y[j].y, acc[i][j]);
-              acc[i][j] = fmaf(x[i].z, y[j].z, acc[i][j]);
-              acc[i][j] = fmaf(x[i].w, y[j].w, acc[i][j]);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int r = r0 + 16 * i, c = c0 + 16 * j, gap = rev ? c - r : r - c;
-            P[r * L::kPP + c] = gap >= 0 && r < n && c < n ? acc[i][j] * pw[gap] : 0.f;
-          }
+      rows_arrived();
+      if (n > 0) {
+        if (rev)
+          scores<D, true>(P, X, Y, pw, n);
+        else
+          scores<D, false>(P, X, Y, pw, n);
       }
       __syncthreads();
-      {
-        constexpr int kCols = D / 4, kRowGroups = kThreads / kCols, kRpt = kC / kRowGroups;
-        const int c = (tid % kCols) * 4, r0 = tid / kCols;
-        float o[kRpt][4];
+      float o[kR][4];
 #pragma unroll
-        for (int i = 0; i < kRpt; ++i)
+      for (int i = 0; i < kR; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-        for (int k = 0; k < D; ++k) {
-          const float4 s = *reinterpret_cast<const float4*>(W + k * D + c);
+        for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+      if (n > 0) {
+        rows_times<kR>(o, X + r0 * L::kPitch, L::kPitch, W + c, D, 0, D);
 #pragma unroll
-          for (int i = 0; i < kRpt; ++i) {
-            const float x = X[(r0 + kRowGroups * i) * L::kPitch + k];
-            o[i][0] = fmaf(x, s.x, o[i][0]);
-            o[i][1] = fmaf(x, s.y, o[i][1]);
-            o[i][2] = fmaf(x, s.z, o[i][2]);
-            o[i][3] = fmaf(x, s.w, o[i][3]);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < kRpt; ++i) {
-          const int r = r0 + kRowGroups * i;
+        for (int i = 0; i < kR; ++i) {
+          const int r = r0 + i;
           const float f = r < n ? pw[rev ? n - 1 - r : r + 1] : 0.f;
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[i][e] *= f;
         }
-        for (int k = 0; k < n; ++k) {
-          const float4 z = *reinterpret_cast<const float4*>(Z + k * L::kPitch + c);
+        // columns of P that these rows see
+        rows_times<kR>(o, P + r0 * L::kPP, L::kPP, Z + c, L::kPitch, rev ? r0 / 4 * 4 : 0,
+                       rev ? (n + 3) / 4 * 4 : min((r0 + kR + 3) / 4 * 4, (n + 3) / 4 * 4));
+      }
+      T* out = static_cast<T*>(jb.o.p) + b * jb.o.sb + h * jb.o.sh;
 #pragma unroll
-          for (int i = 0; i < kRpt; ++i) {
-            const float q = P[(r0 + kRowGroups * i) * L::kPP + k];
-            o[i][0] = fmaf(q, z.x, o[i][0]);
-            o[i][1] = fmaf(q, z.y, o[i][1]);
-            o[i][2] = fmaf(q, z.z, o[i][2]);
-            o[i][3] = fmaf(q, z.w, o[i][3]);
-          }
-        }
-        T* out = static_cast<T*>(jb.o.p) + b * jb.o.sb + h * jb.o.sh;
+      for (int i = 0; i < kR; ++i) {
+        const int r = r0 + i;
+        if (r >= n_rows) continue;
+        float v[4];
 #pragma unroll
-        for (int i = 0; i < kRpt; ++i) {
-          const int r = r0 + kRowGroups * i;
-          if (r >= n_rows) continue;
-          float v[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = r < n ? p.alpha * o[i][e] : 0.f;
-          store4(out + (long long)(row0 + r) * jb.o.sn + c, v);
-        }
+        for (int e = 0; e < 4; ++e) v[e] = r < n ? p.alpha * o[i][e] : 0.f;
+        store4(out + (long long)(row0 + r) * jb.o.sn + c, v);
       }
       __syncthreads();
-      if (n > 0) update_state<D>(W, Y, Z, w, pw[n], n);
+      const bool more = u + 1 < pc.u1;
+      if (more) load_rows<T, D>(X, jb.x, b, h, first_row(u + 1), rows_of(u + 1));
+      if (n > 0) {
+        StateTile<D> S;
+        S.zero();
+        S.add(Y, Z, w, n);
+        const float fall = pw[n];
+#pragma unroll
+        for (int i = 0; i < S.kT; ++i)
+#pragma unroll
+          for (int j = 0; j < S.kT; ++j) {
+            float* q = W + S.at(tid >> 4, i) * D + S.at(tid & 15, j);
+            *q = fmaf(fall, *q, S.a[i][j]);
+          }
+      }
+      __syncthreads();
+      if (more) {
+        load_rows<T, D>(Y, jb.y, b, h, first_row(u + 1), rows_of(u + 1));
+        load_rows<T, D>(Z, jb.z, b, h, first_row(u + 1), rows_of(u + 1));
+      }
     }
     if (pc.u1 == pl.nc && jb.final_out) {
-      __syncthreads();
       float* dst = jb.final_out + b * jb.final_stride + (long long)h * D * D;
       for (int i = tid; i < D * D; i += kThreads)
         dst[jb.transposed ? (i % D) * D + i / D : i] = jb.final_mul * W[i];
@@ -347,6 +420,10 @@ cudaError_t launch_lin_out_simt(const LinOutParams& p, int D, int fp32, cudaStre
   if (D == 32) return fp32 ? out_simt<float, 32>(p, st) : out_simt<__nv_bfloat16, 32>(p, st);
   if (D == 64) return fp32 ? out_simt<float, 64>(p, st) : out_simt<__nv_bfloat16, 64>(p, st);
   return fp32 ? out_simt<float, 128>(p, st) : out_simt<__nv_bfloat16, 128>(p, st);
+}
+
+int lin_simt_ctas(int D) {
+  return kLinSms * (D == 32 ? SimtLayout<32>::kCtas : D == 64 ? SimtLayout<64>::kCtas : SimtLayout<128>::kCtas);
 }
 
 cudaError_t launch_lin_scan(const LinStateParams& p, int D, cudaStream_t st) {

@@ -36,7 +36,7 @@ namespace vdn {
 constexpr int kLinSms = 148;          // CTAs a wave holds (one for each SM of a B200)
 constexpr int kLinMaxGrid = 2 * kLinSms;  // most ranges of a split plan
 constexpr int kLinMaxSub = 4;             // most pieces of a range's part
-constexpr int kLinSimtChunk = 32;     // rows of a chunk: fp32 kernels
+constexpr int kLinSimtChunk = 64;     // rows of a chunk: fp32 kernels
 constexpr int kLinTcChunk = 128;      // rows of a chunk: tensor-core kernels
 
 struct LinView {
@@ -156,6 +156,7 @@ cudaError_t launch_lin_states_simt(const LinStateParams& p, int D, int fp32, cud
 cudaError_t launch_lin_states_tc(const LinTcMaps& m, const LinStateParams& p, cudaStream_t st);
 cudaError_t launch_lin_out_tc(const LinTcMaps& m, const LinOutParams& p, cudaStream_t st);
 bool make_lin_map(LinMap* m, const LinView& v, int B, int N, int H, int d, bool output);
+int lin_simt_ctas(int D);  // CTAs of launch_lin_out_simt that run at once
 cudaError_t launch_lin_scan(const LinStateParams& p, int D, cudaStream_t st);
 cudaError_t launch_lin_out_simt(const LinOutParams& p, int D, int fp32, cudaStream_t st);
 cudaError_t launch_lin_step(const LinStepParams& p, int D, int fp32, cudaStream_t st);
