@@ -516,10 +516,16 @@ def _match(name, t, like):
         raise ValueError(f"{name}: the elements of the last dimension must be contiguous")
 
 
-def _view(name, t, like) -> bytes:
-    """Packed view of a [B, N, H, d] or (a step's) [B, H, d] tensor, checked against ``like``."""
+def _new(like):
+    """A contiguous tensor of the shape, type and device of ``like``."""
+    return torch.empty_like(like, memory_format=torch.contiguous_format)
+
+
+def _view(name, t, like, shape, dtype, index) -> bytes:
+    """Packed view of a [B, N, H, d] or (a step's) [B, H, d] tensor, checked against ``like``, whose shape, type and device
+    number follow."""
     s = t.stride()
-    if t.shape != like.shape or t.dtype != like.dtype or t.device != like.device or s[-1] != 1:
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index or s[-1] != 1:
         _match(name, t, like)
     return _VIEW(t.data_ptr(), s[0], s[1], s[2]) if len(s) == 4 else _VIEW(t.data_ptr(), s[0], 0, s[1])
 
@@ -604,8 +610,9 @@ def linear_attn_fwd(q, k, v, log_decay, *, scale: float = 0.0, state_in=None, st
         B, N, H, d = _sizes(q, 4)
         dev = q.device
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        a, b, c, o = _view("q", q, q), _view("k", k, q), _view("v", v, q), _view("out", out, q)
+            out = _new(q)
+        like = (q, q.shape, q.dtype, q.get_device())
+        a, b, c, o = _view("q", q, *like), _view("k", k, *like), _view("v", v, *like), _view("out", out, *like)
         s_in, s_in_stride = _state("state_in", state_in, B, H, d, dev)
         s_out, s_out_stride = _state("state_out", state_out, B, H, d, dev)
         ws = _scratch(workspace, _linear_bytes(B, N, H, d, q.dtype), dev)
@@ -627,9 +634,10 @@ def linear_attn_bwd(q, k, v, log_decay, d_out, *, scale: float = 0.0, state_in=N
     with _on(q, stream):
         B, N, H, d = _sizes(q, 4)
         dev = q.device
-        dq, dk, dv = (torch.empty(q.shape, dtype=q.dtype, device=dev) if t is None else t for t in (dq, dk, dv))
-        views = [_view(n, t, q) for n, t in (("q", q), ("k", k), ("v", v), ("d_out", d_out), ("dq", dq), ("dk", dk),
-                                             ("dv", dv))]
+        dq, dk, dv = (_new(q) if t is None else t for t in (dq, dk, dv))
+        like = (q, q.shape, q.dtype, q.get_device())
+        views = [_view(n, t, *like) for n, t in (("q", q), ("k", k), ("v", v), ("d_out", d_out), ("dq", dq), ("dk", dk),
+                                                 ("dv", dv))]
         s_in, s_in_stride = _state("state_in", state_in, B, H, d, dev)
         ds_out, ds_out_stride = _state("d_state_out", d_state_out, B, H, d, dev)
         ds_in, ds_in_stride = _state("d_state_in", d_state_in, B, H, d, dev)
@@ -655,8 +663,9 @@ def linear_attn_step(q, k, v, log_decay, state, *, slots=None, scale: float = 0.
         B, H, d = _sizes(q, 3)
         dev = q.device
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        a, b, c, o = _view("q", q, q), _view("k", k, q), _view("v", v, q), _view("out", out, q)
+            out = _new(q)
+        like = (q, q.shape, q.dtype, q.get_device())
+        a, b, c, o = _view("q", q, *like), _view("k", k, *like), _view("v", v, *like), _view("out", out, *like)
         n = state.shape[0]
         pool, slot_stride = _state("state", state, n, H, d, dev)
         cfg = _LINEAR(B, 0, H, d, _DTYPES[q.dtype], scale, _flat("log_decay", log_decay, H, torch.float32, dev), 0, 0,
@@ -719,14 +728,14 @@ def add_rmsnorm_fwd(x, weight=None, *, residual=None, residual_out=None, eps: fl
             kind = torch.float8_e4m3fn
             groups = 1 if out_mode == NORM_OUT_E4M3_ROW else (W + 127) // 128
             if scales is None:
-                scales = torch.empty((rows, groups), dtype=torch.float32, device=dev)
+                scales = torch.empty_strided((rows, groups), (groups, 1), dtype=torch.float32, device=dev)
             elif scales.shape != (rows, groups) or scales.dtype != torch.float32 or scales.device != dev \
                     or not scales.is_contiguous():
                 raise ValueError(f"scales: expected a contiguous {(rows, groups)} torch.float32 on {dev}, got "
                                  f"{tuple(scales.shape)} {scales.dtype} on {scales.device}")
             ps = scales.data_ptr()
         if out is None:
-            out = torch.empty(x.shape, dtype=kind, device=dev)
+            out = torch.empty_like(x, dtype=kind, memory_format=torch.contiguous_format)
         px, x_stride = _rows("x", x, x, x.dtype)
         pr, r_stride = _rows("residual", residual, x, x.dtype)
         ph, h_stride = _rows("residual_out", residual_out, x, x.dtype)
@@ -747,7 +756,7 @@ def add_rmsnorm_bwd(h, weight, dy, *, dh=None, eps: float = -1.0, dx=None, dweig
         rows, W = _matrix(h)
         dev = h.device
         if dx is None:
-            dx = torch.empty(h.shape, dtype=h.dtype, device=dev)
+            dx = _new(h)
         pw = ws_ptr = ws_bytes = 0
         if not want_dweight:
             dweight = None
