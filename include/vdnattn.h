@@ -336,9 +336,9 @@ VDN_API vdn_status vdn_hybrid_attn_fwd_host(const void* q, const void* k, const 
  *   vdn_linear_attn_step  one token of each of `batch` sequences, on a pool of
  *                         states that is updated in place.
  *
- * log_decay is expected to be <= 0 (-infinity: lambda = 0, a token sees itself
- * only); larger values follow the formula.  It is a constant of the model: no
- * gradient by it is formed.
+ * log_decay is finite or -infinity (lambda = 0, a token sees itself only), and
+ * expected to be <= 0; larger values follow the formula.  It is a constant of
+ * the model: no gradient by it is formed.
  *
  * Accumulation, states and decay factors are fp32.  fp32 tensors are computed
  * in fp32 throughout.  The contractions of bf16 tensors run on the tensor
@@ -355,7 +355,7 @@ VDN_API vdn_status vdn_hybrid_attn_fwd_host(const void* q, const void* k, const 
  * slices of one projection.  data is 16-byte aligned and every stride a
  * multiple of 16 bytes; an input's stride may be 0 (a broadcast), an output's
  * only where that dimension has one entry.  Outputs must not overlap each other
- * or an input.
+ * or an input (the same address is refused, other overlaps are not seen).
  *
  * lengths (optional, device, one int32 per batch entry, clamped to [0, tokens]):
  * batch entry b has lengths[b] tokens, and its later rows are padding.  Padding
@@ -442,8 +442,9 @@ VDN_API vdn_status vdn_linear_attn_step(const vdn_view* q, const vdn_view* k, co
  *
  * Row strides in elements, any value >= width; pointers aligned to their
  * element.  Rows that are 16-byte aligned with a width divisible by 8 take
- * vector loads.  x may be residual_out or, with VDN_NORM_TENSOR, out; outputs
- * must not overlap otherwise.  There is no counterpart on the article's pages
+ * vector loads.  x or residual may be residual_out or, with VDN_NORM_TENSOR, out,
+ * and dh may be dx, with the same strides; outputs must not overlap otherwise (the
+ * same address is refused where it is not allowed, other overlaps are not seen).  There is no counterpart on the article's pages
  * (its RMSNorm of the linear read is part of vdn_hybrid_attn_fwd).
  * ---------------------------------------------------------------------- */
 

@@ -351,3 +351,53 @@ def test_no_tokens():
     assert (s1 == 0).all()
     vb.linear_attn_bwd(q, q, q, ld, q, d_state_out=s0, d_state_in=s1)
     assert torch.equal(s0, s1)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("B,N,H,d", [(400, 3, 2, 64), (90, 200, 4, 128), (1, 130, 301, 32), (37, 129, 8, 64)])
+def test_many_short_heads(B, N, H, d, dtype):
+    """More heads than CTAs: a CTA goes through several, padded and empty ones among them."""
+    q, k, v, do = tensors(B, N, H, d, dtype, names="qkvo")
+    ld, s0, ds = decays(H), states(B, H, d, 5), states(B, H, d, 6)
+    n = torch.arange(B, device="cuda", dtype=torch.int32) * 7919 % (N + 1)
+    ref = R.forward(q, k, v, ld, d ** -0.5, s0, n)
+    state, din = s0.clone(), torch.empty_like(s0)
+    out = vb.linear_attn_fwd(q, k, v, ld, state_in=state, state_out=state, lengths=n, debug_flags=vb.POISON_WS)
+    R.check(out, ref["out"], "out", dtype, d, N)
+    R.check(state, ref["state"], "state", dtype, d, N)
+    ref = R.backward(q, k, v, ld, d ** -0.5, do, s0, ds, n)
+    grads = vb.linear_attn_bwd(q, k, v, ld, do, state_in=s0, d_state_out=ds, d_state_in=din, lengths=n)
+    for name, got in zip(("dq", "dk", "dv", "d_state_in"), (*grads, din)):
+        R.check(got, ref[name], name, dtype, d, N)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+def test_broadcast_inputs(dtype):
+    """One query for all batch entries, one value for all heads; states that share memory are refused."""
+    B, N, H, d = 3, 200, 2, 64
+    q = tensors(1, N, H, d, dtype)[0].expand(B, N, H, d)
+    k = tensors(B, N, H, d, dtype, seed=1)[0]
+    v = tensors(B, N, 1, d, dtype, seed=2)[0].expand(B, N, H, d)
+    ld = decays(H)
+    ref = R.forward(q, k, v, ld, 0.5)
+    R.check(vb.linear_attn_fwd(q, k, v, ld, scale=0.5), ref["out"], "out", dtype, d, N)
+    one = states(1, H, d, 1).expand(B, H, d, d)
+    for kw in (dict(state_in=one), dict(state_out=one)):
+        with pytest.raises(ValueError):
+            vb.linear_attn_fwd(q, k, v, ld, **kw)
+    with pytest.raises(ValueError):
+        vb.linear_attn_step(q[:, 0], k[:, 0], v[:, 0], ld, one)
+    with pytest.raises(ValueError):
+        vb.linear_attn_bwd(q, k, v, ld, k, d_state_in=one)
+
+
+def test_growing_memory():
+    """log_decay > 0 follows the formula."""
+    B, N, H, d = 1, 300, 2, 64
+    ld = torch.tensor([0.01, 0.1], device="cuda")
+    for dtype in (BF16, FP32):
+        q, k, v = tensors(B, N, H, d, dtype)
+        ref = R.forward(q, k, v, ld, 0.1)
+        state = torch.empty(B, H, d, d, device="cuda")
+        R.check(vb.linear_attn_fwd(q, k, v, ld, scale=0.1, state_out=state), ref["out"], "out", dtype, d, N)
+        R.check(state, ref["state"], "state", dtype, d, N)

@@ -182,3 +182,24 @@ def test_packed_forms_match_the_structures(struct, pack):
     assert len(b) == ctypes.sizeof(struct)
     s = struct.from_buffer_copy(b)
     assert [getattr(s, f[0]) for f in struct._fields_] == values
+
+
+def test_outputs_that_are_inputs_are_refused():
+    lib, c = vb.library(), cfg(state_out=P, n_slots=2)
+    t = [view((i + 1) << 24) for i in range(7)]
+    for i in range(3):
+        a = t[:3] + [t[i]]
+        assert lib.vdn_linear_attn_fwd(*a, ctypes.byref(c), None) == 1
+        assert lib.vdn_linear_attn_step(*a, ctypes.byref(c), None) == 1
+    for o in (4, 5, 6):
+        for i in [0, 1, 2, 3] + [x for x in (4, 5, 6) if x != o]:
+            a = list(t)
+            a[o] = t[i]
+            assert lib.vdn_linear_attn_bwd(*a, ctypes.byref(c), None) == 1
+    Q = 1 << 24
+    assert lib.vdn_add_rmsnorm_fwd(P, None, Q, Q, None, ctypes.byref(norm()), None) == 1
+    e4m3 = norm(output=vb.NORM_OUT_E4M3_GROUP)
+    assert lib.vdn_add_rmsnorm_fwd(P, None, None, P, Q, ctypes.byref(e4m3), None) == 1
+    assert lib.vdn_add_rmsnorm_fwd(P, Q, None, Q, P, ctypes.byref(e4m3), None) == 1
+    for h, dy in ((Q, P), (P, Q)):
+        assert lib.vdn_add_rmsnorm_bwd(h, dy, None, Q, None, ctypes.byref(norm()), None) == 1

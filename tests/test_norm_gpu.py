@@ -146,6 +146,9 @@ def test_in_place(W):
     c = x.clone()
     vb.add_rmsnorm_fwd(c, None, residual=res, out=c)
     assert torch.equal(c, want)
+    want, dw = vb.add_rmsnorm_bwd(x, None, res, dh=b)
+    dx, dw2 = vb.add_rmsnorm_bwd(x, None, res, dh=b, dx=b)
+    assert dx is b and torch.equal(dx, want) and torch.equal(dw, dw2)
 
 
 @pytest.mark.parametrize("W", [100, 256, 2048, 40000])

@@ -540,6 +540,8 @@ def _state(name, t, B, H, d, device):
     s = t.stride()
     if s[1:] != (d * d, d, 1) and (H > 1 or s[2:] != (d, 1)):
         raise ValueError(f"{name}: the last three dimensions must be contiguous")
+    if B > 1 and s[0] < H * d * d:
+        raise ValueError(f"{name}: states must not overlap (an expanded state: copy it)")
     return t.data_ptr(), s[0] if B > 1 else 0
 
 
@@ -714,7 +716,7 @@ def add_rmsnorm_fwd(x, weight=None, *, residual=None, residual_out=None, eps: fl
 
     x, residual, residual_out: [rows, W], bf16 or fp32, any row stride;
     residual_out, where given, receives h in the tensors' type (it may be x or
-    residual); weight: [W] fp32 or None (ones).  Returns y in the tensors' type,
+    residual, as may out in the tensors' type); weight: [W] fp32 or None (ones).  Returns y in the tensors' type,
     or, for NORM_OUT_E4M3_ROW / NORM_OUT_E4M3_GROUP, (values, scales): e4m3
     [rows, W] and fp32 scales [rows, 1] / [rows, ceil(W / 128)], y ~ value *
     scale."""
@@ -751,7 +753,7 @@ def add_rmsnorm_bwd(h, weight, dy, *, dh=None, eps: float = -1.0, dx=None, dweig
     """Gradients (dx, dweight) of :func:`add_rmsnorm_fwd` with the tensor output:
     dx, by x and equally by residual, in the tensors' type, and dweight [W] fp32
     (None unless ``want_dweight``).  h: the stored residual_out (or x); dh: the
-    gradient that reaches h from elsewhere, or None."""
+    gradient that reaches h from elsewhere, or None (dx may be dh)."""
     with _on(h, stream):
         rows, W = _matrix(h)
         dev = h.device

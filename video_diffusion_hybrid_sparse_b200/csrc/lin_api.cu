@@ -54,6 +54,14 @@ vdn_status check_common(const vdn_linear_cfg* c) {
   return VDN_OK;
 }
 
+// An output that is an input (any other overlap is the caller's to avoid).
+bool same_data(std::initializer_list<const vdn_view*> outputs, std::initializer_list<const vdn_view*> inputs) {
+  for (const vdn_view* o : outputs)
+    for (const vdn_view* x : inputs)
+      if (o->data == x->data) return true;
+  return false;
+}
+
 // A tensor's view: `step`: the token stride is not used.
 vdn_status check_view(const vdn_linear_cfg* c, const vdn_view* v, bool output, bool step = false) {
   if (!v || !v->data) return VDN_ERR_INVALID_ARG;
@@ -94,10 +102,11 @@ LinPlan make_plan(const vdn_linear_cfg* c, int jobs, int walks, bool tc) {
   const long long heads = (long long)c->batch * c->heads;
   pl.total = heads * pl.nc;
   const int per_wave = tc ? kLinSms : lin_simt_ctas(c->head_dim);
-  const long long whole = (heads * jobs + per_wave - 1) / per_wave * pl.nc;
+  const int most = per_wave / jobs;
+  const long long whole = (heads + most - 1) / most * pl.nc;
   const long long parts = (pl.total * (2 * jobs + walks) + 2 * per_wave - 1) / (2 * per_wave) + 8;
   pl.split = parts < whole;
-  pl.grid = pl.split ? (int)std::min<long long>(per_wave / jobs, pl.total) : (int)heads;
+  pl.grid = (int)std::min<long long>(most, pl.split ? pl.total : heads);
   // a range's part in up to four pieces, of eight chunks at least
   pl.sub = pl.split ? (int)std::max<long long>(1, std::min<long long>(kLinMaxSub, pl.total / pl.grid / 8)) : 1;
   return pl;
@@ -215,6 +224,7 @@ vdn_status vdn_linear_attn_fwd(const vdn_view* q, const vdn_view* k, const vdn_v
   const LinPlan pl = make_plan(cfg, 1, 1, tc);
   const LinLayout l = make_layout(cfg, pl, 1, true);
   if ((s = check_ws(cfg, l.total)) != VDN_OK) return s;
+  if (cfg->tokens > 0 && same_data({out}, {q, k, v})) return VDN_ERR_INVALID_ARG;
   if (cfg->tokens == 0)
     return cuda_status(copy_states(cfg, cfg->state_out, out_stride, cfg->state_in, in_stride, st));
   if (poison(cfg, l.total, st) != cudaSuccess) return VDN_ERR_CUDA;
@@ -271,6 +281,9 @@ vdn_status vdn_linear_attn_bwd(const vdn_view* q, const vdn_view* k, const vdn_v
   const LinPlan pl = make_plan(cfg, 3, 2, tc);
   const LinLayout l = make_layout(cfg, pl, 2, false);
   if ((s = check_ws(cfg, l.total)) != VDN_OK) return s;
+  if (cfg->tokens > 0 &&
+      (same_data({dq, dk, dv}, {q, k, v, d_out}) || same_data({dq}, {dk, dv}) || same_data({dk}, {dv})))
+    return VDN_ERR_INVALID_ARG;
   if (cfg->tokens == 0)
     return cuda_status(copy_states(cfg, cfg->d_state_in, din_stride, cfg->d_state_out, dout_stride, st));
   if (poison(cfg, l.total, st) != cudaSuccess) return VDN_ERR_CUDA;
@@ -319,6 +332,7 @@ vdn_status vdn_linear_attn_step(const vdn_view* q, const vdn_view* k, const vdn_
   for (const vdn_view* x : {q, k, v})
     if ((s = check_view(cfg, x, false, true)) != VDN_OK) return s;
   if ((s = check_view(cfg, out, true, true)) != VDN_OK) return s;
+  if (same_data({out}, {q, k, v})) return VDN_ERR_INVALID_ARG;
   LinStepParams p;
   std::memset(&p, 0, sizeof(p));
   p.q = view(q), p.k = view(k), p.v = view(v), p.o = view(out);
@@ -379,6 +393,8 @@ vdn_status vdn_add_rmsnorm_fwd(const void* x, const void* residual, void* residu
   for (const void* p : {x, residual, (const void*)residual_out, quant ? nullptr : (const void*)out})
     if (!aligned(p, e)) return VDN_ERR_ALIGNMENT;
   if (!aligned(cfg->weight, 4) || !aligned(scales, 4)) return VDN_ERR_ALIGNMENT;
+  // out may be x or residual where a thread reads what it overwrites; residual_out may be either in every mode
+  if (out == residual_out || (quant && (out == x || out == residual))) return VDN_ERR_INVALID_ARG;
   NormParams p;
   p.x = x, p.res = residual, p.res_out = residual_out, p.out = out, p.scales = scales, p.weight = cfg->weight;
   p.rows = cfg->rows, p.W = cfg->width;
@@ -401,7 +417,7 @@ vdn_status vdn_add_rmsnorm_bwd(const void* h, const void* dy, const void* dh, vo
   if (cfg->output != VDN_NORM_TENSOR) return VDN_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int e = cfg->dtype == VDN_FP32 ? 4 : 2;
-  if (cfg->rows > 0 && (!h || !dy || !dx)) return VDN_ERR_INVALID_ARG;
+  if (cfg->rows > 0 && (!h || !dy || !dx )) return VDN_ERR_INVALID_ARG;
   for (const void* p : {h, dy, dh, (const void*)dx})
     if (!aligned(p, e)) return VDN_ERR_ALIGNMENT;
   if (!aligned(cfg->weight, 4) || !aligned(dweight, 4)) return VDN_ERR_ALIGNMENT;
@@ -409,6 +425,7 @@ vdn_status vdn_add_rmsnorm_bwd(const void* h, const void* dy, const void* dh, vo
     if (!cfg->workspace || cfg->workspace_bytes < vdn_norm_workspace_bytes(cfg)) return VDN_ERR_WORKSPACE;
     if (!aligned(cfg->workspace, 256)) return VDN_ERR_ALIGNMENT;
   }
+  if (cfg->rows > 0 && (dx == h || dx == dy)) return VDN_ERR_INVALID_ARG;
   if (cfg->rows == 0) return dweight ? cuda_status(cudaMemsetAsync(dweight, 0, (size_t)cfg->width * 4, st)) : VDN_OK;
   NormBwdParams p;
   p.h = h, p.dy = dy, p.dh = dh, p.dx = dx, p.dweight = dweight, p.weight = cfg->weight;

@@ -54,7 +54,8 @@ struct LinTcMaps {
 };
 
 // The chunks of every (batch, head), (batch, head)-major and in walk order,
-// form one list; CTA j takes [start(j), start(j + 1)).  Where a range begins
+// form one list; CTA j takes [start(j), start(j + 1)): whole heads, as many as
+// make one wave of CTAs, or equal parts.  Where a range begins
 // inside a head, the state before it is the sum of what the earlier ranges of
 // that head leave: each range's own share ("part") is formed by a first kernel,
 // a scan over the ranges adds them up, and the walk starts from the result.
@@ -66,8 +67,8 @@ struct LinPlan {
   int sub;          // pieces of a range's part, each formed by a CTA of its own
   long long total;  // chunks of all heads
 
-  VDN_HD long long start(int j) const { return total * j / grid; }
-  // the range that holds chunk t of the list
+  VDN_HD long long start(int j) const { return split ? total * j / grid : total / nc * j / grid * nc; }
+  // the range that holds chunk t of the list (equal parts)
   VDN_HD int range_of(long long t) const { return (int)(((t + 1) * grid + total - 1) / total - 1); }
 };
 
