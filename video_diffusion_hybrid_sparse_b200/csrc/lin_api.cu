@@ -107,8 +107,9 @@ LinPlan make_plan(const vdn_linear_cfg* c, int jobs, int walks, bool tc) {
   const long long parts = (pl.total * (2 * jobs + walks) + 2 * per_wave - 1) / (2 * per_wave) + 8;
   pl.split = parts < whole;
   pl.grid = (int)std::min<long long>(most, pl.split ? pl.total : heads);
-  // a range's part in up to four pieces, of eight chunks at least
-  pl.sub = pl.split ? (int)std::max<long long>(1, std::min<long long>(kLinMaxSub, pl.total / pl.grid / 8)) : 1;
+  // a range's part in one, two or four pieces, of eight chunks at least
+  const long long eights = pl.split ? pl.total / pl.grid / 8 : 1;
+  pl.sub = eights >= 4 ? kLinMaxSub : eights >= 2 ? 2 : 1;
   return pl;
 }
 

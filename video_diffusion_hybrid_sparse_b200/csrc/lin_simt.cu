@@ -333,15 +333,19 @@ __global__ void __launch_bounds__(kThreads) lin_out_simt(const __grid_constant__
 
 // State before each range that begins inside a head: s_in[j] = lambda^rows(j - 1)
 // s_in[j - 1] + part[j - 1] along the head's ranges, from the state before the
-// walk.  A thread owns four elements and goes through the ranges.  Bound by the
-// latency of its loads, which do not depend on one another: eight are in flight.
+// walk.  A thread owns kE elements and goes through the ranges.  Bound by the
+// latency of its loads, which do not depend on one another: 8 or 16 are in
+// flight.  Few heads take one element a thread, for more threads (four heads of
+// 128 x 128 in 148 pieces each: 45 us with four, which suffice from some hundred
+// threads an SM on).
+template <int kE>
 __global__ void __launch_bounds__(128) lin_scan(const __grid_constant__ LinStateParams p, int DD) {
-  constexpr int kAhead = 8;
+  constexpr int kAhead = kE == 4 ? 8 : 16;
   const LinPlan& pl = p.pl;
   const LinWalk& wk = p.walk[blockIdx.y];
   pdl_release();
-  const int per = (DD + 4 * (int)blockDim.x - 1) / (4 * (int)blockDim.x);  // blocks of a head
-  const int bh = blockIdx.x / per, b = bh / p.H, h = bh % p.H, sub = pl.sub;
+  const int per = (DD + kE * (int)blockDim.x - 1) / (kE * (int)blockDim.x);  // blocks of a head
+  const int bh = blockIdx.x / per, b = bh / p.H, h = bh % p.H, sub = pl.sub, lg = sub == 4 ? 2 : sub - 1;
   const long long head0 = (long long)bh * pl.nc;
   const int j0 = pl.range_of(head0), j1 = pl.range_of(head0 + pl.nc - 1);
   if (j1 == j0) return;
@@ -352,37 +356,50 @@ __global__ void __launch_bounds__(128) lin_scan(const __grid_constant__ LinState
   __shared__ bool has[kLinMaxGrid * kLinMaxSub];
   const int n = (j1 - j0) * sub;
   for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    const int j = j0 + i / sub;
-    const LinStretch st = lin_piece_of(lin_stretch(j, len, l2, pl, wk.reverse), i % sub, pl);
+    const int j = j0 + (i >> lg);
+    const LinStretch st = lin_piece_of(lin_stretch(j, len, l2, pl, wk.reverse), i & (sub - 1), pl);
     has[i] = st.u0 < st.u1;
-    if (i % sub == 0)
-      fall[i / sub] = lin_pow(l2, lin_rows((int)(max(pl.start(j), head0) - head0), (int)(pl.start(j + 1) - head0), len, pl, wk.reverse));
+    if ((i & (sub - 1)) == 0)
+      fall[i >> lg] = lin_pow(l2, lin_rows((int)(max(pl.start(j), head0) - head0), (int)(pl.start(j + 1) - head0), len, pl, wk.reverse));
   }
   __syncthreads();
   pdl_wait();
-  const int e = (blockIdx.x % per * blockDim.x + threadIdx.x) * 4;
+  const int e = (blockIdx.x % per * blockDim.x + threadIdx.x) * kE;
   if (e >= DD) return;
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (wk.init) {
-    s = *reinterpret_cast<const float4*>(wk.init + b * wk.init_stride + (long long)h * DD + e);
-    s = make_float4(s.x * wk.init_mul, s.y * wk.init_mul, s.z * wk.init_mul, s.w * wk.init_mul);
-  }
-  if (wk.s_head) *reinterpret_cast<float4*>(wk.s_head + (long long)j0 * DD + e) = s;
-  for (int i0 = 0; i0 < n; i0 += kAhead) {
-    float4 a[kAhead];
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      a[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (i0 + i < n && has[i0 + i])
-        a[i] = *reinterpret_cast<const float4*>(wk.parts + ((long long)j0 * sub + i0 + i) * DD + e);
+  auto load = [](float (&f)[kE], const float* q) {
+    if constexpr (kE == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(q);
+      f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+    } else {
+      f[0] = *q;
     }
+  };
+  auto store = [](float* q, const float (&f)[kE]) {
+    if constexpr (kE == 4)
+      *reinterpret_cast<float4*>(q) = make_float4(f[0], f[1], f[2], f[3]);
+    else
+      *q = f[0];
+  };
+  float s[kE] = {};
+  if (wk.init) {
+    load(s, wk.init + b * wk.init_stride + (long long)h * DD + e);
+#pragma unroll
+    for (int x = 0; x < kE; ++x) s[x] *= wk.init_mul;
+  }
+  if (wk.s_head) store(wk.s_head + (long long)j0 * DD + e, s);
+  for (int i0 = 0; i0 < n; i0 += kAhead) {
+    float a[kAhead][kE] = {};
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (i0 + i < n && has[i0 + i]) load(a[i], wk.parts + ((long long)j0 * sub + i0 + i) * DD + e);
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       if (i0 + i >= n) continue;
-      const int k = (i0 + i) / sub;
-      if (i0 + i == k * sub) s = make_float4(fall[k] * s.x, fall[k] * s.y, fall[k] * s.z, fall[k] * s.w);
-      s = make_float4(s.x + a[i].x, s.y + a[i].y, s.z + a[i].z, s.w + a[i].w);
-      if (i0 + i == k * sub + sub - 1) *reinterpret_cast<float4*>(wk.s_in + (long long)(j0 + k + 1) * DD + e) = s;
+      const int k = (i0 + i) >> lg, part = (i0 + i) & (sub - 1);
+      const float f = part == 0 ? fall[k] : 1.f;
+#pragma unroll
+      for (int x = 0; x < kE; ++x) s[x] = fmaf(f, s[x], a[i][x]);
+      if (part == sub - 1) store(wk.s_in + (long long)(j0 + k + 1) * DD + e, s);
     }
   }
 }
@@ -427,7 +444,10 @@ int lin_simt_ctas(int D) {
 }
 
 cudaError_t launch_lin_scan(const LinStateParams& p, int D, cudaStream_t st) {
-  return launch_after(lin_scan, dim3((D * D + 511) / 512 * p.B * p.H, p.n_walks), 128, 0, st, p, D * D);
+  const int DD = D * D, heads = p.B * p.H;
+  if ((long long)DD / 4 * heads * p.n_walks >= kLinSms * 512)
+    return launch_after(lin_scan<4>, dim3((DD + 511) / 512 * heads, p.n_walks), 128, 0, st, p, DD);
+  return launch_after(lin_scan<1>, dim3((DD + 127) / 128 * heads, p.n_walks), 128, 0, st, p, DD);
 }
 
 }  // namespace vdn

@@ -64,7 +64,7 @@ struct LinPlan {
   int nc;           // chunks of a head
   int grid;         // ranges
   int split;        // a range may begin inside a head
-  int sub;          // pieces of a range's part, each formed by a CTA of its own
+  int sub;          // pieces of a range's part, each formed by itself: 1, 2 or 4
   long long total;  // chunks of all heads
 
   VDN_HD long long start(int j) const { return split ? total * j / grid : total / nc * j / grid * nc; }
