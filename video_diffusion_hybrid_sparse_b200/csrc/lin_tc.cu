@@ -14,16 +14,22 @@
 // state is kept in two or three bf16 parts (16 or 24 bits), because a state is
 // read by every later token.
 //
-// Bound by memory: a chunk reads three tiles and writes one (128 KB at
-// head_dim 128: 2.9 us of a 148th of the HBM rate) against 2560 cycles of
-// products; TMA keeps the next chunk's tiles in flight in a ring of slots.
+// A chunk reads three tiles and writes one (128 KB at head_dim 128: 2.9 us of a
+// 148th of the HBM rate, 5200 cycles) against 2560 cycles of products; TMA keeps
+// the next chunk's tiles in flight in a ring of slots.  Measured: 7000 cycles at
+// 128 columns, 4700 at 64 (241920 x 4 x 128: 213 us; the scan and the parts of
+// the ranges beside).  Bound by shared memory, 85 % of its cycles at 128
+// columns, and by the issue of the warps' instructions, 0.60-0.63 a cycle.
+//
 // Roles (28 warps): warp 0 TMA, warps 1-2 issue the products, warps 4-19 decay
 // (P in TMEM, then Y: its first part in place, the others beside), warps 20-27
 // write the output rows and carry W (a thread owns half a row of W).  TMEM is
 // full: S | O1 | O2 | dW, 128 columns each; P overwrites S's columns in place.
 // Two warps issue, P Z and the next chunk's scores in turn, X W and dW in turn:
 // W of this chunk is published while P Z and the scores run, Y decayed while
-// all three do, and the next P made during dW.
+// all three do, and the next P made during dW.  (S and dW twice, which 64
+// columns have room for, made a chunk longer: 277 us instead of 211 at 8 x 10000
+// x 16 x 64.)
 //
 // Products of 128 x 128 x 16 from shared memory take all its bandwidth (8 KB in
 // 64 cycles), so that every other access lengthens the chunk: arrivals are one
@@ -32,9 +38,9 @@
 // of W does not see; three: 3e-7, as fp32 sums are).
 //
 // The roles' loops run at once and share an instruction cache of about 32 KB:
-// loops over products, rows and tiles stay rolled and waits are short, or the
-// one warp that issues products waits for its instructions.  (Unrolled, 110 KB
-// of code: 11000 cycles a chunk.)
+// loops over halves and rows stay rolled and waits are short.  The products are
+// unrolled all the same: their operands are then made in uniform registers (5-8
+// % of the call).
 //
 // head_dim 32 takes the 64-column form: TMA fills the upper columns with
 // zeros, so that DRAM traffic stays that of 32.
@@ -82,9 +88,7 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
-// A value the compiler takes for a new one: what is made from it is not kept from one turn of a loop to the next.  (A
-// descriptor kept that way is a register of 48, and a spilled one a read that often goes to L2, as shared memory leaves
-// little L1: such reads once cost 300 cycles a product.)
+// A value the compiler takes for a new one: it stays in a register and is not read again from the parameters.
 __device__ __forceinline__ uint32_t fresh(uint32_t v) {
   asm volatile("" : "+r"(v));
   return v;
@@ -256,8 +260,9 @@ __device__ __forceinline__ void mma_columns(uint32_t acc, uint32_t a, uint32_t b
   }
 }
 
-// dW (+)= (Y1 + Y2 + ..)^T Z over 64 rows of a chunk, of n_parts parts: y, z at their first row, parts as decay_half leaves them (D = 64:
-// rows 64-127 of the transposed operand are the zero block, which stays where it is from one 16-row step to the next)
+// dW (+)= (Y1 + Y2 + ..)^T Z over 64 rows of a chunk, of n_parts parts: y, z at their first row, parts as decay_half leaves
+// them (D = 64: rows 64-127 of the transposed operand are the zero block, which stays where it is from one 16-row step to
+// the next)
 template <int D>
 __device__ __forceinline__ void mma_state(uint32_t acc, uint32_t y, uint32_t parts, uint32_t zero, uint32_t z, uint32_t go,
                                           int n_parts) {
