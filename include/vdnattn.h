@@ -345,7 +345,8 @@ VDN_API vdn_status vdn_hybrid_attn_fwd_host(const void* q, const void* k, const 
  * cores: decayed scores and the state are rounded to bf16 as operands of the
  * read (not in the carried state), and decayed keys enter the state in two or
  * three bf16 parts (2^-16 of a term, 2^-24 of one whose decay to the end is
- * above 2^-4).  A token's contribution may end where its decay has fallen below
+ * above 2^-4 where the last state is asked for: out and dv may differ in their
+ * rounding with it).  A token's contribution may end where its decay has fallen below
  * 2^-150.  A NaN or an infinity in a real token's row may reach earlier rows of
  * its 128-row chunk too.
  *

@@ -401,3 +401,57 @@ def test_growing_memory():
         state = torch.empty(B, H, d, d, device="cuda")
         R.check(vb.linear_attn_fwd(q, k, v, ld, scale=0.1, state_out=state), ref["out"], "out", dtype, d, N)
         R.check(state, ref["state"], "state", dtype, d, N)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+def test_both_ways_of_a_call(dtype):
+    """Calls made in one step and those that go through the binding's own checks (here: with a stream or a workspace given)
+    are the same calls."""
+    B, N, H, d = 2, 300, 2, 64
+    q, k, v, do = tensors(B, N, H, d, dtype, packed=True, names="qkvo")
+    ld, s0, n = decays(H), states(B, H, d, 1), torch.tensor([300, 17], dtype=torch.int32, device="cuda")
+    here = torch.cuda.current_stream()
+    last = [torch.empty_like(s0) for _ in range(2)]
+    a = vb.linear_attn_fwd(q, k, v, ld, state_in=s0, state_out=last[0], lengths=n, scale=0.2)
+    b = vb.linear_attn_fwd(q, k, v, ld, state_in=s0, state_out=last[1], lengths=n, scale=0.2, stream=here)
+    assert torch.equal(a, b) and torch.equal(*last) and a.is_contiguous() and a.stride() == b.stride()
+    ws = torch.empty(vb.linear_workspace_bytes(B, N, H, d, dtype, True), dtype=torch.uint8, device="cuda")
+    a = vb.linear_attn_bwd(q, k, v, ld, do, state_in=s0, d_state_out=s0, d_state_in=last[0], lengths=n)
+    b = vb.linear_attn_bwd(q, k, v, ld, do, state_in=s0, d_state_out=s0, d_state_in=last[1], lengths=n, workspace=ws)
+    assert all(torch.equal(x, y) for x, y in zip(a, b)) and torch.equal(*last)
+    into = [torch.empty(B, N, H, d, device="cuda", dtype=dtype) for _ in range(3)]
+    c = vb.linear_attn_bwd(q, k, v, ld, do, state_in=s0, d_state_out=s0, d_state_in=last[1], lengths=n, dq=into[0],
+                           dk=into[1], dv=into[2])
+    assert all(x.data_ptr() == y.data_ptr() and torch.equal(x, z) for x, y, z in zip(c, into, a))
+    pools = [states(5, H, d, 2), states(5, H, d, 2)]
+    slots = torch.tensor([3, 1], dtype=torch.int32, device="cuda")
+    a = vb.linear_attn_step(q[:, 0], k[:, 0], v[:, 0], ld, pools[0], slots=slots)
+    b = vb.linear_attn_step(q[:, 0], k[:, 0], v[:, 0], ld, pools[1], slots=slots, stream=here)
+    assert torch.equal(a, b) and torch.equal(*pools)
+
+
+def test_binding_refuses_what_does_not_fit():
+    B, N, H, d = 2, 40, 2, 64
+    q, k, v = tensors(B, N, H, d, BF16)
+    ld, s0 = decays(H), states(B, H, d, 1)
+    for args, kw in (((q, k[:, :-1], v, ld), {}), ((q, k.float(), v, ld), {}), ((q, k, v, ld.double()), {}),
+                     ((q, k, v, ld[:1]), {}), ((q, k, v, ld.cpu()), {}), ((q, k, v, ld), dict(state_in=s0[:1])),
+                     ((q, k, v, ld), dict(state_in=s0.transpose(2, 3))), ((q, k, v, ld), dict(state_out=s0.bfloat16())),
+                     ((q, k, v, ld), dict(lengths=torch.tensor([1, 2], device="cuda"))),
+                     ((q, k, v, ld), dict(out=torch.empty_like(q, dtype=FP32))), ((q[0], k[0], v[0], ld), {}),
+                     ((q, k, v.transpose(1, 3).contiguous().transpose(1, 3), ld), {})):
+        with pytest.raises(ValueError):
+            vb.linear_attn_fwd(*args, **kw)
+    with pytest.raises(vb.VdnError):
+        vb.linear_attn_fwd(*(t[..., :48] for t in (q, k, v)), ld)
+    with pytest.raises(vb.VdnError):  # the output is an input
+        vb.linear_attn_fwd(q, k, v, ld, out=k)
+    with pytest.raises(vb.VdnError):
+        wide = torch.empty(B, N, H, d + 1, device="cuda", dtype=BF16)[..., :d]
+        vb.linear_attn_fwd(wide, k, v, ld)
+    with pytest.raises(ValueError):
+        vb.linear_attn_step(q[:, 0], k[:, 0], v[:, 0], ld, s0, slots=torch.tensor([0], dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError):
+        vb.linear_attn_step(q[:, 0], k[:, 0], v[:, 0], ld, s0[:, :1])
+    with pytest.raises(vb.VdnError):  # fewer entries than rows
+        vb.linear_attn_step(q[:, 0], k[:, 0], v[:, 0], ld, s0[:1])

@@ -210,6 +210,30 @@ def test_tiny_scales_and_empty():
     assert dx.shape == (0, 128) and (dw == 0).all()
 
 
+def test_both_ways_of_a_call_and_refusals():
+    """Calls made in one step and those that go through the binding's own checks (a stream given) are the same calls."""
+    x, res, dy = (rows_of(6, 300, BF16, i) for i in (1, 2, 3))
+    gamma, here = 1.0 + 0.2 * rows_of(1, 300, FP32, 3)[0], torch.cuda.current_stream()
+    for mode in (vb.NORM_OUT_TENSOR, vb.NORM_OUT_E4M3_ROW, vb.NORM_OUT_E4M3_GROUP):
+        a, b = (vb.add_rmsnorm_fwd(x, gamma, residual=res, out_mode=mode, **kw) for kw in ({}, dict(stream=here)))
+        for s, t in zip(*((r if isinstance(r, tuple) else (r,)) for r in (a, b))):
+            assert s.dtype == t.dtype and torch.equal(s.float(), t.float())
+    a, b = (vb.add_rmsnorm_bwd(x, gamma, dy, dh=res, **kw) for kw in ({}, dict(stream=here)))
+    assert all(torch.equal(s, t) for s, t in zip(a, b))
+    for f in (lambda: vb.add_rmsnorm_fwd(x, gamma[:-1]), lambda: vb.add_rmsnorm_fwd(x, gamma.bfloat16()),
+              lambda: vb.add_rmsnorm_fwd(x, residual=res[:, 1:]), lambda: vb.add_rmsnorm_fwd(x, residual=res.float()),
+              lambda: vb.add_rmsnorm_fwd(x[0]), lambda: vb.add_rmsnorm_fwd(x.half()), lambda: vb.add_rmsnorm_fwd(x.t()),
+              lambda: vb.add_rmsnorm_fwd(x, out=torch.empty_like(x, dtype=FP32)),
+              lambda: vb.add_rmsnorm_fwd(x, residual_out=x[:1].expand(6, 300)),
+              lambda: vb.add_rmsnorm_fwd(x, out_mode=1, scales=torch.empty(6, device="cuda")),
+              lambda: vb.add_rmsnorm_bwd(x, gamma, dy[:-1]), lambda: vb.add_rmsnorm_bwd(x, gamma, dy, dweight=gamma[1:])):
+        with pytest.raises(ValueError):
+            f()
+    for f in (lambda: vb.add_rmsnorm_fwd(x, out_mode=3), lambda: vb.add_rmsnorm_bwd(x, gamma, dy, dx=dy)):
+        with pytest.raises(vb.VdnError):
+            f()
+
+
 def test_streams_graphs_and_repeats():
     x, dy = rows_of(3000, 2048, BF16, 1), rows_of(3000, 2048, BF16, 2)
     gamma = 1.0 + 0.2 * rows_of(1, 2048, FP32, 3)[0]

@@ -484,6 +484,21 @@ def validate(s: Shape, **kw) -> int:
 NORM_OUT_TENSOR, NORM_OUT_E4M3_ROW, NORM_OUT_E4M3_GROUP = 0, 1, 2
 _DTYPES = {torch.bfloat16: VDN_BF16, torch.float32: VDN_FP32}
 _HERE = contextlib.nullcontext()
+_calls = None  # the extension module of csrc/py/calls.cpp
+
+
+def _direct():
+    """The module that makes ordinary calls in one step (csrc/py/calls.cpp): each
+    of its functions returns None for a call that it leaves to the code here."""
+    global _calls
+    if _calls is None:
+        library()
+        from . import _calls as module
+
+        _calls = module
+    return _calls
+
+
 # the fields of VdnView, VdnLinearCfg and VdnNormCfg in their order
 _VIEW = struct.Struct("@P3q").pack
 _LINEAR = struct.Struct("@5if6P4qP2iPNP").pack
@@ -581,8 +596,15 @@ def linear_workspace_bytes(B: int, N: int, H: int, d: int, dtype=torch.bfloat16,
     return n
 
 
-# sizes only: nothing of a call's tensors
+# of sizes only: nothing of a call's tensors is kept
 _linear_bytes = functools.lru_cache(maxsize=256)(linear_workspace_bytes)
+
+
+def _made(r, where):
+    """The outputs of a call made in one step, or its error."""
+    if r.__class__ is int:
+        _check(r, where)
+    return r
 
 
 def _scratch(workspace, n, device):
@@ -608,6 +630,10 @@ def linear_attn_fwd(q, k, v, log_decay, *, scale: float = 0.0, state_in=None, st
     state_in, state_out: [B, H, d, d] fp32 or None, state_out is written and may
     be state_in; lengths: [B] int32 or None, the tokens of each padded sequence:
     rows behind them come out as zeros.  ``scale`` <= 0 selects d**-0.5."""
+    if stream is None and workspace is None:
+        r = _direct().linear_fwd(q, k, v, log_decay, scale, state_in, state_out, lengths, out, status, debug_flags)
+        if r is not None:
+            return _made(r, "vdn_linear_attn_fwd")
     with _on(q, stream):
         B, N, H, d = _sizes(q, 4)
         dev = q.device
@@ -633,6 +659,11 @@ def linear_attn_bwd(q, k, v, log_decay, d_out, *, scale: float = 0.0, state_in=N
     state ([B, H, d, d] fp32); ``d_state_in``, where given, receives the gradient
     by state_in.  Nothing of the forward call is kept: q, k, v and state_in are
     read again.  Rows behind ``lengths`` get zeros."""
+    if stream is None and workspace is None:
+        r = _direct().linear_bwd(q, k, v, log_decay, d_out, scale, state_in, d_state_out, d_state_in, lengths, dq, dk, dv,
+                                 status, debug_flags)
+        if r is not None:
+            return _made(r, "vdn_linear_attn_bwd")
     with _on(q, stream):
         B, N, H, d = _sizes(q, 4)
         dev = q.device
@@ -661,6 +692,10 @@ def linear_attn_step(q, k, v, log_decay, state, *, slots=None, scale: float = 0.
     b).  A negative slot marks a padding row (out is zero there, no state is
     touched), and so does one past the pool, which also sets ``status`` (int32) to
     1.  Rows of the same slot are successive tokens, in the order of the rows."""
+    if stream is None:
+        r = _direct().linear_step(q, k, v, log_decay, state, slots, scale, out, status)
+        if r is not None:
+            return _made(r, "vdn_linear_attn_step")
     with _on(q, stream):
         B, H, d = _sizes(q, 3)
         dev = q.device
@@ -720,6 +755,10 @@ def add_rmsnorm_fwd(x, weight=None, *, residual=None, residual_out=None, eps: fl
     or, for NORM_OUT_E4M3_ROW / NORM_OUT_E4M3_GROUP, (values, scales): e4m3
     [rows, W] and fp32 scales [rows, 1] / [rows, ceil(W / 128)], y ~ value *
     scale."""
+    if stream is None:
+        r = _direct().norm_fwd(x, weight, residual, residual_out, eps, out_mode, out, scales)
+        if r is not None:
+            return _made(r, "vdn_add_rmsnorm_fwd")
     with _on(x, stream):
         rows, W = _matrix(x)
         dev = x.device
@@ -754,6 +793,10 @@ def add_rmsnorm_bwd(h, weight, dy, *, dh=None, eps: float = -1.0, dx=None, dweig
     dx, by x and equally by residual, in the tensors' type, and dweight [W] fp32
     (None unless ``want_dweight``).  h: the stored residual_out (or x); dh: the
     gradient that reaches h from elsewhere, or None (dx may be dh)."""
+    if stream is None and workspace is None:
+        r = _direct().norm_bwd(h, weight, dy, dh, eps, dx, dweight, want_dweight)
+        if r is not None:
+            return _made(r, "vdn_add_rmsnorm_bwd")
     with _on(h, stream):
         rows, W = _matrix(h)
         dev = h.device

@@ -1,9 +1,10 @@
-"""Build libvdnattn.so in-tree with nvcc for sm_100a.
+"""Build libvdnattn.so in-tree with nvcc for sm_100a, and the binding's _calls.so with g++.
 
     python -m video_diffusion_hybrid_sparse_b200.build [--force] [--verbose]
 
-Objects go to ``_build/`` next to this file; the shared library is written
-next to this file so that it travels with the source tree.
+Objects go to ``_build/`` next to this file; the shared libraries are written
+next to this file so that they travel with the source tree.  ``_calls.so`` is
+built against the headers of the installed torch.
 """
 from __future__ import annotations
 
@@ -13,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -21,6 +23,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libvdnattn.so")
+CALLS = os.path.join(PKG, "_calls.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -85,7 +88,32 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         if r.returncode != 0:
             sys.stderr.write(r.stdout + r.stderr)
             raise RuntimeError("link failed")
+    build_calls(force, verbose)
     return LIB
+
+
+def build_calls(force: bool = False, verbose: bool = False) -> str:
+    """The extension module that makes the binding's small calls (csrc/py/calls.cpp)."""
+    import torch
+    from torch.utils import cpp_extension
+
+    src, header = os.path.join(CSRC, "py", "calls.cpp"), os.path.join(INCLUDE, "vdnattn.h")
+    if not force and not _stale(CALLS, [src, header, torch.__file__]):
+        return CALLS
+    home = os.path.dirname(os.path.dirname(nvcc()))
+    dirs = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"], os.path.join(home, "include"), INCLUDE]
+    libs = cpp_extension.library_paths()
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden", "-Wno-attributes",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-I{d}" for d in dirs], src, "-o", CALLS,
+           f"-L{PKG}", "-l:libvdnattn.so", "-Wl,-rpath,$ORIGIN", *[f"-L{d}" for d in libs], "-lc10", "-lc10_cuda",
+           "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("the binding's extension module failed to build")
+    return CALLS
 
 
 def main():
