@@ -118,7 +118,7 @@ struct WaitRecord {
 
 static_assert(kNumBars * 8 + 8 + sizeof(WaitRecord) <= 272, "barrier block");
 
-// A probe that may suspend the warp for a while: 26 warps that probe in a loop are shared-memory traffic.
+// A probe may suspend the warp until the phase completes, so that a wait seldom probes twice.
 constexpr uint32_t kSuspendNs = 100000;
 // mbar_wait in few instructions (see the head of the file): the same bound in global time, read at every probe.
 __device__ __forceinline__ bool try_wait_long(uint64_t* bar, uint32_t parity) {
@@ -294,7 +294,8 @@ __device__ __forceinline__ void store_wait() { asm volatile("cp.async.bulk.wait_
 namespace {
 
 // Whether the third part of the decayed Y counts in a state that is handed out (or on): in chunks whose weight there,
-// `rows` rows later, is above 2^-4 (without decay the first part is Y itself).  What is left out is below 2^-16 of a term, and 2^-20 of terms of weight one.
+// `rows` rows later, is above 2^-4 (without decay the first part is Y itself).  What is left out is below 2^-16 of a term,
+// and 2^-20 of terms of weight one.
 __device__ __forceinline__ bool third_part(float l2, int rows) { return l2 != 0.f && l2 * (float)rows > -4.f; }
 
 }  // namespace
