@@ -175,15 +175,6 @@ def test_workspace_follows_the_split():
         vb.linear_workspace_bytes(1, 10, 1, 40)
 
 
-@pytest.mark.parametrize("struct,pack", [(vb.VdnView, vb._VIEW), (vb.VdnLinearCfg, vb._LINEAR), (vb.VdnNormCfg, vb._NORM)])
-def test_packed_forms_match_the_structures(struct, pack):
-    values = [i + 1 for i in range(len(struct._fields_))]
-    b = pack(*values)
-    assert len(b) == ctypes.sizeof(struct)
-    s = struct.from_buffer_copy(b)
-    assert [getattr(s, f[0]) for f in struct._fields_] == values
-
-
 def test_outputs_that_are_inputs_are_refused():
     lib, c = vb.library(), cfg(state_out=P, n_slots=2)
     t = [view((i + 1) << 24) for i in range(7)]

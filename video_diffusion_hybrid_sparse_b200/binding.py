@@ -11,7 +11,6 @@ import contextlib
 import ctypes
 import functools
 import os
-import struct
 from dataclasses import dataclass
 
 import numpy as np
@@ -19,7 +18,6 @@ import torch
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libvdnattn.so")
 _lib = None
-_lib_packed = None
 
 VDN_BF16, VDN_FP32 = 0, 1
 OUT_SOFTMAX_ONLY, OUT_LINEAR_ONLY, OUT_LINEAR_RAW, EXPORT_STATES, INJECT_TIMEOUT = 1, 2, 4, 8, 16
@@ -139,24 +137,6 @@ def library() -> ctypes.CDLL:
                 getattr(lib, name).restype = ctypes.c_int
         _lib = lib
     return _lib
-
-
-def _packed() -> ctypes.CDLL:
-    """The calls of the linear memory and of the norm with views and configs as
-    packed bytes: filling a ctypes structure field by field takes longer than
-    the smallest of these calls run."""
-    global _lib_packed
-    if _lib_packed is None:
-        library()
-        lib = ctypes.CDLL(_LIB_PATH)
-        P, S = ctypes.c_void_p, ctypes.c_char_p
-        lib.vdn_linear_attn_fwd.argtypes = [S, S, S, S, S, P]
-        lib.vdn_linear_attn_bwd.argtypes = [S, S, S, S, S, S, S, S, P]
-        lib.vdn_linear_attn_step.argtypes = [S, S, S, S, S, P]
-        lib.vdn_add_rmsnorm_fwd.argtypes = [P, P, P, P, P, S, P]
-        lib.vdn_add_rmsnorm_bwd.argtypes = [P, P, P, P, P, S, P]
-        _lib_packed = lib
-    return _lib_packed
 
 
 @dataclass
@@ -499,12 +479,6 @@ def _direct():
     return _calls
 
 
-# the fields of VdnView, VdnLinearCfg and VdnNormCfg in their order
-_VIEW = struct.Struct("@P3q").pack
-_LINEAR = struct.Struct("@5if6P4qP2iPNP").pack
-_NORM = struct.Struct("@q3if P7qPN").pack
-
-
 def _on(t: torch.Tensor, stream):
     """Context in which a call on ``t`` allocates and launches: its device, and
     ``stream`` (of that device) when one is given."""
@@ -536,13 +510,13 @@ def _new(like):
     return torch.empty_like(like, memory_format=torch.contiguous_format)
 
 
-def _view(name, t, like, shape, dtype, index) -> bytes:
-    """Packed view of a [B, N, H, d] or (a step's) [B, H, d] tensor, checked against ``like``, whose shape, type and device
+def _view(name, t, like, shape, dtype, index) -> VdnView:
+    """View of a [B, N, H, d] or (a step's) [B, H, d] tensor, checked against ``like``, whose shape, type and device
     number follow."""
     s = t.stride()
     if t.shape != shape or t.dtype is not dtype or t.get_device() != index or s[-1] != 1:
         _match(name, t, like)
-    return _VIEW(t.data_ptr(), s[0], s[1], s[2]) if len(s) == 4 else _VIEW(t.data_ptr(), s[0], 0, s[1])
+    return VdnView(t.data_ptr(), s[0], s[1], s[2]) if len(s) == 4 else VdnView(t.data_ptr(), s[0], 0, s[1])
 
 
 def _state(name, t, B, H, d, device):
@@ -644,10 +618,10 @@ def linear_attn_fwd(q, k, v, log_decay, *, scale: float = 0.0, state_in=None, st
         s_in, s_in_stride = _state("state_in", state_in, B, H, d, dev)
         s_out, s_out_stride = _state("state_out", state_out, B, H, d, dev)
         ws = _scratch(workspace, _linear_bytes(B, N, H, d, q.dtype), dev)
-        cfg = _LINEAR(B, N, H, d, _DTYPES[q.dtype], scale, _flat("log_decay", log_decay, H, torch.float32, dev),
+        cfg = VdnLinearCfg(B, N, H, d, _DTYPES[q.dtype], scale, _flat("log_decay", log_decay, H, torch.float32, dev),
                       _flat("lengths", lengths, B, torch.int32, dev), s_in, s_out, 0, 0, s_in_stride, s_out_stride, 0, 0,
                       0, 0, debug_flags, ws.data_ptr(), ws.nbytes, _word("status", status, dev))
-        _check(_packed().vdn_linear_attn_fwd(a, b, c, o, cfg, _here(q)), "vdn_linear_attn_fwd")
+        _check(library().vdn_linear_attn_fwd(a, b, c, o, ctypes.byref(cfg), _here(q)), "vdn_linear_attn_fwd")
     return out
 
 
@@ -675,11 +649,11 @@ def linear_attn_bwd(q, k, v, log_decay, d_out, *, scale: float = 0.0, state_in=N
         ds_out, ds_out_stride = _state("d_state_out", d_state_out, B, H, d, dev)
         ds_in, ds_in_stride = _state("d_state_in", d_state_in, B, H, d, dev)
         ws = _scratch(workspace, _linear_bytes(B, N, H, d, q.dtype, True), dev)
-        cfg = _LINEAR(B, N, H, d, _DTYPES[q.dtype], scale, _flat("log_decay", log_decay, H, torch.float32, dev),
+        cfg = VdnLinearCfg(B, N, H, d, _DTYPES[q.dtype], scale, _flat("log_decay", log_decay, H, torch.float32, dev),
                       _flat("lengths", lengths, B, torch.int32, dev), s_in, 0, ds_out, ds_in, s_in_stride, 0,
                       ds_out_stride, ds_in_stride, 0, 0, debug_flags, ws.data_ptr(), ws.nbytes,
                       _word("status", status, dev))
-        _check(_packed().vdn_linear_attn_bwd(*views, cfg, _here(q)), "vdn_linear_attn_bwd")
+        _check(library().vdn_linear_attn_bwd(*views, ctypes.byref(cfg), _here(q)), "vdn_linear_attn_bwd")
     return dq, dk, dv
 
 
@@ -705,10 +679,10 @@ def linear_attn_step(q, k, v, log_decay, state, *, slots=None, scale: float = 0.
         a, b, c, o = _view("q", q, *like), _view("k", k, *like), _view("v", v, *like), _view("out", out, *like)
         n = state.shape[0]
         pool, slot_stride = _state("state", state, n, H, d, dev)
-        cfg = _LINEAR(B, 0, H, d, _DTYPES[q.dtype], scale, _flat("log_decay", log_decay, H, torch.float32, dev), 0, 0,
+        cfg = VdnLinearCfg(B, 0, H, d, _DTYPES[q.dtype], scale, _flat("log_decay", log_decay, H, torch.float32, dev), 0, 0,
                       pool, 0, 0, 0, slot_stride, 0, 0, _flat("slots", slots, B, torch.int32, dev), n, 0, 0, 0,
                       _word("status", status, dev))
-        _check(_packed().vdn_linear_attn_step(a, b, c, o, cfg, _here(q)), "vdn_linear_attn_step")
+        _check(library().vdn_linear_attn_step(a, b, c, o, ctypes.byref(cfg), _here(q)), "vdn_linear_attn_step")
     return out
 
 
@@ -781,9 +755,9 @@ def add_rmsnorm_fwd(x, weight=None, *, residual=None, residual_out=None, eps: fl
         pr, r_stride = _rows("residual", residual, x, x.dtype)
         ph, h_stride = _rows("residual_out", residual_out, x, x.dtype)
         po, o_stride = _rows("out", out, x, kind)
-        cfg = _NORM(rows, W, _DTYPES[x.dtype], out_mode, eps, _flat("weight", weight, W, torch.float32, dev), x_stride,
+        cfg = VdnNormCfg(rows, W, _DTYPES[x.dtype], out_mode, eps, _flat("weight", weight, W, torch.float32, dev), x_stride,
                     r_stride, h_stride, o_stride, 0, 0, 0, 0, 0)
-        _check(_packed().vdn_add_rmsnorm_fwd(px, pr, ph, po, ps, cfg, _here(x)), "vdn_add_rmsnorm_fwd")
+        _check(library().vdn_add_rmsnorm_fwd(px, pr, ph, po, ps, ctypes.byref(cfg), _here(x)), "vdn_add_rmsnorm_fwd")
     return out if ps == 0 and kind is x.dtype else (out, scales)
 
 
@@ -815,7 +789,7 @@ def add_rmsnorm_bwd(h, weight, dy, *, dh=None, eps: float = -1.0, dx=None, dweig
         pdy, dy_stride = _rows("dy", dy, h, h.dtype)
         pdh, dh_stride = _rows("dh", dh, h, h.dtype)
         pdx, dx_stride = _rows("dx", dx, h, h.dtype)
-        cfg = _NORM(rows, W, _DTYPES[h.dtype], 0, eps, _flat("weight", weight, W, torch.float32, dev), h_stride, 0, 0, 0,
+        cfg = VdnNormCfg(rows, W, _DTYPES[h.dtype], 0, eps, _flat("weight", weight, W, torch.float32, dev), h_stride, 0, 0, 0,
                     dy_stride, dh_stride, dx_stride, ws_ptr, ws_bytes)
-        _check(_packed().vdn_add_rmsnorm_bwd(ph, pdy, pdh, pdx, pw, cfg, _here(h)), "vdn_add_rmsnorm_bwd")
+        _check(library().vdn_add_rmsnorm_bwd(ph, pdy, pdh, pdx, pw, ctypes.byref(cfg), _here(h)), "vdn_add_rmsnorm_bwd")
     return dx, dweight
