@@ -102,6 +102,18 @@ bool sizes(const Arg& q, int dims, vdn_linear_cfg* c) {
 
 PyObject* none() { Py_RETURN_NONE; }
 
+// Other Python threads go on while this one allocates and launches (a full launch queue makes it wait for the device).
+class Released {
+ public:
+  Released() : state_(PyEval_SaveThread()) {}
+  ~Released() { PyEval_RestoreThread(state_); }
+  Released(const Released&) = delete;
+  Released& operator=(const Released&) = delete;
+
+ private:
+  PyThreadState* state_;
+};
+
 // q, k, v, log_decay, scale, state_in, state_out, lengths, out, status, debug_flags
 PyObject* linear_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -125,10 +137,16 @@ PyObject* linear_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   c.status_word = static_cast<int32_t*>(status.ptr());
   c.workspace_bytes = vdn_linear_workspace_bytes(&c, 0);
   if (c.workspace_bytes == 0) return none();
-  const Tensor ws = scratch(c.workspace_bytes, *q.t), made = out.t ? *out.t : new_like(*q.t);
-  c.workspace = ws.data_ptr();
-  if (!out.t) x[3] = vdn_view{made.data_ptr(), made.stride(0), made.stride(1), made.stride(2)};
-  const vdn_status r = vdn_linear_attn_fwd(&x[0], &x[1], &x[2], &x[3], &c, stream_of(*q.t));
+  Tensor made;
+  vdn_status r;
+  {
+    Released others;
+    const Tensor ws = scratch(c.workspace_bytes, *q.t);
+    made = out.t ? *out.t : new_like(*q.t);
+    c.workspace = ws.data_ptr();
+    if (!out.t) x[3] = vdn_view{made.data_ptr(), made.stride(0), made.stride(1), made.stride(2)};
+    r = vdn_linear_attn_fwd(&x[0], &x[1], &x[2], &x[3], &c, stream_of(*q.t));
+  }
   return r == VDN_OK ? THPVariable_Wrap(made) : PyLong_FromLong(r);
   END_HANDLE_TH_ERRORS
 }
@@ -159,14 +177,18 @@ PyObject* linear_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   c.status_word = static_cast<int32_t*>(status.ptr());
   c.workspace_bytes = vdn_linear_workspace_bytes(&c, 1);
   if (c.workspace_bytes == 0) return none();
-  const Tensor ws = scratch(c.workspace_bytes, *q.t);
-  c.workspace = ws.data_ptr();
   Tensor made[3];
-  for (int i = 0; i < 3; ++i) {
-    made[i] = g[i].t ? *g[i].t : new_like(*q.t);
-    if (!g[i].t) x[4 + i] = vdn_view{made[i].data_ptr(), made[i].stride(0), made[i].stride(1), made[i].stride(2)};
+  vdn_status r;
+  {
+    Released others;
+    const Tensor ws = scratch(c.workspace_bytes, *q.t);
+    c.workspace = ws.data_ptr();
+    for (int i = 0; i < 3; ++i) {
+      made[i] = g[i].t ? *g[i].t : new_like(*q.t);
+      if (!g[i].t) x[4 + i] = vdn_view{made[i].data_ptr(), made[i].stride(0), made[i].stride(1), made[i].stride(2)};
+    }
+    r = vdn_linear_attn_bwd(&x[0], &x[1], &x[2], &x[3], &x[4], &x[5], &x[6], &c, stream_of(*q.t));
   }
-  const vdn_status r = vdn_linear_attn_bwd(&x[0], &x[1], &x[2], &x[3], &x[4], &x[5], &x[6], &c, stream_of(*q.t));
   if (r != VDN_OK) return PyLong_FromLong(r);
   return Py_BuildValue("(NNN)", THPVariable_Wrap(made[0]), THPVariable_Wrap(made[1]), THPVariable_Wrap(made[2]));
   END_HANDLE_TH_ERRORS
@@ -192,9 +214,14 @@ PyObject* linear_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
   c.slots = static_cast<const int32_t*>(slots.ptr());
   c.n_slots = (int32_t)pool.t->size(0);
   c.status_word = static_cast<int32_t*>(status.ptr());
-  const Tensor made = out.t ? *out.t : new_like(*q.t);
-  if (!out.t) x[3] = vdn_view{made.data_ptr(), made.stride(0), 0, made.stride(1)};
-  const vdn_status r = vdn_linear_attn_step(&x[0], &x[1], &x[2], &x[3], &c, stream_of(*q.t));
+  Tensor made;
+  vdn_status r;
+  {
+    Released others;
+    made = out.t ? *out.t : new_like(*q.t);
+    if (!out.t) x[3] = vdn_view{made.data_ptr(), made.stride(0), 0, made.stride(1)};
+    r = vdn_linear_attn_step(&x[0], &x[1], &x[2], &x[3], &c, stream_of(*q.t));
+  }
   return r == VDN_OK ? THPVariable_Wrap(made) : PyLong_FromLong(r);
   END_HANDLE_TH_ERRORS
 }
@@ -239,22 +266,26 @@ PyObject* norm_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!matrix(x, *x.t, x.t->scalar_type(), &c.x_stride) || !matrix(res, *x.t, x.t->scalar_type(), &c.residual_stride) ||
       !matrix(res_out, *x.t, x.t->scalar_type(), &c.residual_out_stride) || !matrix(out, *x.t, kind, &c.out_stride))
     return none();
-  Tensor s;
+  Tensor s, made;
+  int64_t groups = 0;
   if (quant) {
-    const int64_t groups = c.output == VDN_NORM_E4M3_ROW ? 1 : (c.width + 127) / 128;
+    groups = c.output == VDN_NORM_E4M3_ROW ? 1 : (c.width + 127) / 128;
     if (!scales.ok) return none();
     if (scales.t) {
       s = *scales.t;
       if (s.dim() != 2 || s.size(0) != c.rows || s.size(1) != groups || s.scalar_type() != at::kFloat ||
           s.device() != x.t->device() || !s.is_contiguous())
         return none();
-    } else {
-      s = at::empty({c.rows, groups}, x.t->options().dtype(at::kFloat));
     }
   }
-  const Tensor made = out.t ? *out.t : at::empty(x.t->sizes(), x.t->options().dtype(kind));
-  const vdn_status r = vdn_add_rmsnorm_fwd(x.ptr(), res.ptr(), res_out.ptr(), made.data_ptr(),
-                                           quant ? static_cast<float*>(s.data_ptr()) : nullptr, &c, stream_of(*x.t));
+  vdn_status r;
+  {
+    Released others;
+    if (quant && !scales.t) s = at::empty({c.rows, groups}, x.t->options().dtype(at::kFloat));
+    made = out.t ? *out.t : at::empty(x.t->sizes(), x.t->options().dtype(kind));
+    r = vdn_add_rmsnorm_fwd(x.ptr(), res.ptr(), res_out.ptr(), made.data_ptr(),
+                            quant ? static_cast<float*>(s.data_ptr()) : nullptr, &c, stream_of(*x.t));
+  }
   if (r != VDN_OK) return PyLong_FromLong(r);
   return quant ? Py_BuildValue("(NN)", THPVariable_Wrap(made), THPVariable_Wrap(s)) : THPVariable_Wrap(made);
   END_HANDLE_TH_ERRORS
@@ -274,17 +305,21 @@ PyObject* norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!matrix(h, *h.t, type, &c.x_stride) || !matrix(dy, *h.t, type, &c.dy_stride) || !matrix(dh, *h.t, type, &c.dh_stride) ||
       !matrix(dx, *h.t, type, &c.dx_stride) || !vector(dweight, c.width, at::kFloat, *h.t))
     return none();
-  Tensor w, ws;
-  if (want) {
-    c.workspace_bytes = vdn_norm_workspace_bytes(&c);
-    if (c.workspace_bytes == 0) return none();
-    ws = scratch(c.workspace_bytes, *h.t);
-    c.workspace = ws.data_ptr();
-    w = dweight.t ? *dweight.t : at::empty({c.width}, h.t->options().dtype(at::kFloat));
+  if (want && (c.workspace_bytes = vdn_norm_workspace_bytes(&c)) == 0) return none();
+  Tensor made, w;
+  vdn_status r;
+  {
+    Released others;
+    Tensor ws;
+    if (want) {
+      ws = scratch(c.workspace_bytes, *h.t);
+      c.workspace = ws.data_ptr();
+      w = dweight.t ? *dweight.t : at::empty({c.width}, h.t->options().dtype(at::kFloat));
+    }
+    made = dx.t ? *dx.t : new_like(*h.t);
+    r = vdn_add_rmsnorm_bwd(h.ptr(), dy.ptr(), dh.ptr(), made.data_ptr(), want ? static_cast<float*>(w.data_ptr()) : nullptr,
+                            &c, stream_of(*h.t));
   }
-  const Tensor made = dx.t ? *dx.t : new_like(*h.t);
-  const vdn_status r = vdn_add_rmsnorm_bwd(h.ptr(), dy.ptr(), dh.ptr(), made.data_ptr(),
-                                           want ? static_cast<float*>(w.data_ptr()) : nullptr, &c, stream_of(*h.t));
   if (r != VDN_OK) return PyLong_FromLong(r);
   if (want) return Py_BuildValue("(NN)", THPVariable_Wrap(made), THPVariable_Wrap(w));
   return Py_BuildValue("(NO)", THPVariable_Wrap(made), Py_None);
