@@ -444,8 +444,9 @@ VDN_API vdn_status vdn_linear_attn_step(const vdn_view* q, const vdn_view* k, co
  * Row strides in elements, any value >= width; pointers aligned to their
  * element.  Rows that are 16-byte aligned with a width divisible by 8 take
  * vector loads.  x or residual may be residual_out or, with VDN_NORM_TENSOR, out,
- * and dh may be dx, with the same strides; outputs must not overlap otherwise (the
- * same address is refused where it is not allowed, other overlaps are not seen).  There is no counterpart on the article's pages
+ * and dh may be dx, with the same strides; outputs must not overlap otherwise
+ * (the same address with another stride, or where it is not allowed, is refused;
+ * other overlaps are not seen).  There is no counterpart on the article's pages
  * (its RMSNorm of the linear read is part of vdn_hybrid_attn_fwd).
  * ---------------------------------------------------------------------- */
 

@@ -353,6 +353,21 @@ def test_no_tokens():
     assert torch.equal(s0, s1)
 
 
+def test_no_tokens_and_states_far_apart():
+    """Batch entries of the states 2 GB apart, which no pitched copy takes."""
+    B, H, d, gap = 2, 1, 32, 1 << 29
+    q = torch.empty(B, 0, H, d, device="cuda", dtype=BF16)
+    far = torch.full((gap + d * d,), 5.0, device="cuda").as_strided((B, H, d, d), (gap, d * d, d, 1))
+    s0, ld = states(B, H, d, 1), decays(H)
+    vb.linear_attn_fwd(q, q, q, ld, state_in=s0, state_out=far)
+    assert torch.equal(far, s0)
+    back = torch.zeros_like(s0)
+    vb.linear_attn_fwd(q, q, q, ld, state_in=far, state_out=back)
+    assert torch.equal(back, s0)
+    vb.linear_attn_fwd(q, q, q, ld, state_out=far)
+    assert (far == 0).all()
+
+
 @pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
 @pytest.mark.parametrize("B,N,H,d", [(400, 3, 2, 64), (90, 200, 4, 128), (1, 130, 301, 32), (37, 129, 8, 64)])
 def test_many_short_heads(B, N, H, d, dtype):

@@ -194,3 +194,15 @@ def test_outputs_that_are_inputs_are_refused():
     assert lib.vdn_add_rmsnorm_fwd(P, Q, None, Q, P, ctypes.byref(e4m3), None) == 1
     for h, dy in ((Q, P), (P, Q)):
         assert lib.vdn_add_rmsnorm_bwd(h, dy, None, Q, None, ctypes.byref(norm()), None) == 1
+
+
+def test_rows_in_place_keep_their_stride():
+    """An output at an input's address has the input's stride."""
+    lib, Q = vb.library(), 1 << 24
+    f, b = lib.vdn_add_rmsnorm_fwd, lib.vdn_add_rmsnorm_bwd
+    W = norm().width
+    for name, args in (("x_stride", (P, None, P, Q)), ("residual_stride", (Q, P, P, 1 << 25)),
+                       ("residual_out_stride", (P, None, P, Q)), ("out_stride", (P, Q, None, P)),
+                       ("residual_stride", (Q, P, None, P))):
+        assert f(*args, None, ctypes.byref(norm(rows=2, **{name: 2 * W})), None) == 1
+    assert b(P, Q, 1 << 25, 1 << 25, None, ctypes.byref(norm(rows=2, dh_stride=2 * W)), None) == 1

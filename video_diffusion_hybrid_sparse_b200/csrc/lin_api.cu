@@ -156,11 +156,18 @@ cudaError_t poison(const vdn_linear_cfg* c, size_t total, cudaStream_t st) {
 cudaError_t copy_states(const vdn_linear_cfg* c, float* dst, long long dst_stride, const float* src,
                         long long src_stride, cudaStream_t st) {
   if (!dst) return cudaSuccess;
-  const size_t row = (size_t)state_size(c) * 4;
-  if (!src) return cudaMemset2DAsync(dst, (size_t)dst_stride * 4, 0, row, (size_t)c->batch, st);
   if (src == dst) return cudaSuccess;
-  return cudaMemcpy2DAsync(dst, (size_t)dst_stride * 4, src, (size_t)src_stride * 4, row, (size_t)c->batch,
-                           cudaMemcpyDeviceToDevice, st);
+  const size_t row = (size_t)state_size(c) * 4;
+  const long long most_pitch = INT32_MAX / 4;  // of the 2D calls, in elements
+  if (dst_stride <= most_pitch && (!src || src_stride <= most_pitch))
+    return src ? cudaMemcpy2DAsync(dst, (size_t)dst_stride * 4, src, (size_t)src_stride * 4, row, (size_t)c->batch,
+                                   cudaMemcpyDeviceToDevice, st)
+               : cudaMemset2DAsync(dst, (size_t)dst_stride * 4, 0, row, (size_t)c->batch, st);
+  cudaError_t e = cudaSuccess;
+  for (int b = 0; b < c->batch && e == cudaSuccess; ++b)
+    e = src ? cudaMemcpyAsync(dst + b * dst_stride, src + b * src_stride, row, cudaMemcpyDeviceToDevice, st)
+            : cudaMemsetAsync(dst + b * dst_stride, 0, row, st);
+  return e;
 }
 
 // The launches of a call; the jobs and walks name its tensors by their place, inputs first.
@@ -373,6 +380,15 @@ namespace {
 
 int64_t stride_or(int64_t s, int32_t width) { return s ? s : width; }
 
+// An output at an input's address whose later rows lie elsewhere: a row would be overwritten before it is read.
+struct Rows {
+  const void* p;
+  int64_t stride;
+};
+bool shifted(const Rows& out, const Rows& in, int64_t rows) {
+  return out.p && out.p == in.p && out.stride != in.stride && rows > 1;
+}
+
 // 16-byte rows of a tensor of `e`-byte elements
 bool vec_rows(const void* p, int64_t stride, int e) {
   return !p || (aligned(p, 16) && stride * e % 16 == 0);
@@ -396,6 +412,11 @@ vdn_status vdn_add_rmsnorm_fwd(const void* x, const void* residual, void* residu
   if (!aligned(cfg->weight, 4) || !aligned(scales, 4)) return VDN_ERR_ALIGNMENT;
   // out may be x or residual where a thread reads what it overwrites; residual_out may be either in every mode
   if (out == residual_out || (quant && (out == x || out == residual))) return VDN_ERR_INVALID_ARG;
+  const int32_t W = cfg->width;
+  for (auto o : {Rows{out, stride_or(cfg->out_stride, W)}, Rows{residual_out, stride_or(cfg->residual_out_stride, W)}})
+    if (shifted(o, Rows{x, stride_or(cfg->x_stride, W)}, cfg->rows) ||
+        shifted(o, Rows{residual, stride_or(cfg->residual_stride, W)}, cfg->rows))
+      return VDN_ERR_INVALID_ARG;
   NormParams p;
   p.x = x, p.res = residual, p.res_out = residual_out, p.out = out, p.scales = scales, p.weight = cfg->weight;
   p.rows = cfg->rows, p.W = cfg->width;
@@ -418,7 +439,7 @@ vdn_status vdn_add_rmsnorm_bwd(const void* h, const void* dy, const void* dh, vo
   if (cfg->output != VDN_NORM_TENSOR) return VDN_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int e = cfg->dtype == VDN_FP32 ? 4 : 2;
-  if (cfg->rows > 0 && (!h || !dy || !dx )) return VDN_ERR_INVALID_ARG;
+  if (cfg->rows > 0 && (!h || !dy || !dx)) return VDN_ERR_INVALID_ARG;
   for (const void* p : {h, dy, dh, (const void*)dx})
     if (!aligned(p, e)) return VDN_ERR_ALIGNMENT;
   if (!aligned(cfg->weight, 4) || !aligned(dweight, 4)) return VDN_ERR_ALIGNMENT;
@@ -427,6 +448,8 @@ vdn_status vdn_add_rmsnorm_bwd(const void* h, const void* dy, const void* dh, vo
     if (!aligned(cfg->workspace, 256)) return VDN_ERR_ALIGNMENT;
   }
   if (cfg->rows > 0 && (dx == h || dx == dy)) return VDN_ERR_INVALID_ARG;
+  if (shifted(Rows{dx, stride_or(cfg->dx_stride, cfg->width)}, Rows{dh, stride_or(cfg->dh_stride, cfg->width)}, cfg->rows))
+    return VDN_ERR_INVALID_ARG;
   if (cfg->rows == 0) return dweight ? cuda_status(cudaMemsetAsync(dweight, 0, (size_t)cfg->width * 4, st)) : VDN_OK;
   NormBwdParams p;
   p.h = h, p.dy = dy, p.dh = dh, p.dx = dx, p.dweight = dweight, p.weight = cfg->weight;
