@@ -155,6 +155,38 @@ def test_padded_batch(N, d, dtype):
     assert torch.equal(state[1], s0[1]) and torch.equal(state[6], s0[6])
 
 
+@pytest.mark.parametrize("dtype,d", [(BF16, 128), (BF16, 64), (FP32, 64), (FP32, 32)])
+@pytest.mark.parametrize("lengths", [
+    [4000, 0, 1, 2500, 3999, 3000],       # cut by cost, ends inside heads
+    [0, 0, 4000, 4000, 4000, 0, 4000],    # sequences without tokens at both ends
+    [4000, 300, 0, 0, 0, 0],              # too few tokens for that: equal parts
+    [0, 0, 0, 0, 0, 0],
+    [4000 - 97 * i for i in range(40)],   # more sequences than are cut so
+], ids=["mixed", "ends", "few", "none", "many"])
+def test_ragged_ranges(lengths, dtype, d):
+    """Padded sequences long enough to be cut into ranges."""
+    B, N, H = len(lengths), 4000, 2 if len(lengths) < 10 else 1
+    n = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    q, k, v, do = tensors(B, N, H, d, dtype, names="qkvo")
+    ld, s0, ds = decays(H), states(B, H, d, 5), states(B, H, d, 6)
+    ref_f = R.forward(q, k, v, ld, d ** -0.5, s0, n)
+    ref_b = R.backward(q, k, v, ld, d ** -0.5, do, s0, ds, n)
+    pad = torch.arange(N, device="cuda")[None, :] >= n[:, None]
+    for t in (q, k, v, do):
+        t[pad] = float("nan")
+    state, din = s0.clone(), torch.empty_like(s0)
+    out = vb.linear_attn_fwd(q, k, v, ld, state_in=state, state_out=state, lengths=n, debug_flags=vb.POISON_WS)
+    grads = vb.linear_attn_bwd(q, k, v, ld, do, state_in=s0, d_state_out=ds, d_state_in=din, lengths=n,
+                               debug_flags=vb.POISON_WS)
+    R.check(out, ref_f["out"], "out", dtype, d, N)
+    R.check(state, ref_f["state"], "state", dtype, d, N)
+    for name, got in zip(("dq", "dk", "dv"), grads):
+        R.check(got, ref_b[name], name, dtype, d, N)
+        assert (got[pad] == 0).all()
+    R.check(din, ref_b["d_state_in"], "d_state_in", dtype, d, N)
+    assert (out[pad] == 0).all()
+
+
 @pytest.mark.parametrize("dtype,N,d", [(BF16, 700, 128), (BF16, 1500, 64), (FP32, 400, 64), (BF16, 400, 32)])
 def test_views_in_place_state_and_guard_rows(dtype, N, d):
     """Slices of a wider tensor in another order of dimensions, a broadcast key, an output inside a larger one (what lies

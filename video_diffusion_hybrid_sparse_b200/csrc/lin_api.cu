@@ -94,8 +94,12 @@ bool on_tensor_cores(const vdn_linear_cfg* c, std::initializer_list<const vdn_vi
 }
 
 // Ranges: whole heads, or equal parts of all heads' chunks, which cost a kernel for the parts' states (`walks` of them,
-// half of a job's work each) and the scan.  In chunks of one CTA, with the two kernels' launches worth about eight.
-LinPlan make_plan(const vdn_linear_cfg* c, int jobs, int walks, bool tc) {
+// half of a job's work each) and the scan.  In chunks of one CTA; the two kernels' launches, and the scan, are worth some
+// (`launches`, from sweeps of 1 to 300 heads of 100 to 4000 tokens: with 8 for all, a call of 8 heads took 66 us instead of
+// 28 at 400 fp32 tokens and 26.9 instead of 17.6 at 1000 bf16 ones; with 4 and 1, 64 heads take 1.2-1.4 times as long).
+// Sequences of a padded batch are taken to fill three quarters of it, which parts make use of (LinCuts) and whole heads do
+// not: gradients at 4 x 3840 x 16 x 128 take 213 us in whole heads whatever the lengths, in parts 128 to 228 us.
+LinPlan make_plan(const vdn_linear_cfg* c, int jobs, int walks, bool tc, bool padded) {
   LinPlan pl;
   pl.chunk = tc ? kLinTcChunk : kLinSimtChunk;
   pl.nc = std::max(1, (c->tokens + pl.chunk - 1) / pl.chunk);
@@ -104,7 +108,9 @@ LinPlan make_plan(const vdn_linear_cfg* c, int jobs, int walks, bool tc) {
   const int per_wave = tc ? kLinSms : lin_simt_ctas(c->head_dim);
   const int most = per_wave / jobs;
   const long long whole = (heads + most - 1) / most * pl.nc;
-  const long long parts = (pl.total * (2 * jobs + walks) + 2 * per_wave - 1) / (2 * per_wave) + 8;
+  const int launches = !tc ? 2 : c->head_dim == 128 ? 6 : 5;
+  const long long work = padded && c->batch <= kLinCutBatch ? pl.total - pl.total / 4 : pl.total;
+  const long long parts = (work * (2 * jobs + walks) + 2 * per_wave - 1) / (2 * per_wave) + launches;
   pl.split = parts < whole;
   pl.grid = (int)std::min<long long>(most, pl.split ? pl.total : heads);
   // a range's part in one, two or four pieces, of eight chunks at least
@@ -201,12 +207,13 @@ vdn_status vdn_linear_validate(const vdn_linear_cfg* cfg) { return check_linear(
 
 size_t vdn_linear_workspace_bytes(const vdn_linear_cfg* cfg, int32_t backward) {
   if (check_linear(cfg) != VDN_OK) return 0;
-  // either form of the kernels may serve a bf16 call
+  // either form of the kernels may serve a bf16 call; lengths may be set or not
   size_t most = 0;
-  for (bool tc : {false, true}) {
-    const LinPlan pl = backward ? make_plan(cfg, 3, 2, tc) : make_plan(cfg, 1, 1, tc);
-    most = std::max(most, make_layout(cfg, pl, backward ? 2 : 1, !backward).total);
-  }
+  for (bool tc : {false, true})
+    for (bool padded : {false, true}) {
+      const LinPlan pl = backward ? make_plan(cfg, 3, 2, tc, padded) : make_plan(cfg, 1, 1, tc, padded);
+      most = std::max(most, make_layout(cfg, pl, backward ? 2 : 1, !backward).total);
+    }
   return most;
 }
 
@@ -229,7 +236,7 @@ vdn_status vdn_linear_attn_fwd(const vdn_view* q, const vdn_view* k, const vdn_v
     if ((s = check_view(cfg, out, true)) != VDN_OK) return s;
   }
   const bool tc = cfg->tokens > 0 && on_tensor_cores(cfg, {q, k, v});
-  const LinPlan pl = make_plan(cfg, 1, 1, tc);
+  const LinPlan pl = make_plan(cfg, 1, 1, tc, cfg->lengths);
   const LinLayout l = make_layout(cfg, pl, 1, true);
   if ((s = check_ws(cfg, l.total)) != VDN_OK) return s;
   if (cfg->tokens > 0 && same_data({out}, {q, k, v})) return VDN_ERR_INVALID_ARG;
@@ -286,7 +293,7 @@ vdn_status vdn_linear_attn_bwd(const vdn_view* q, const vdn_view* k, const vdn_v
       if ((s = check_view(cfg, x, true)) != VDN_OK) return s;
   }
   const bool tc = cfg->tokens > 0 && on_tensor_cores(cfg, {q, k, v, d_out});
-  const LinPlan pl = make_plan(cfg, 3, 2, tc);
+  const LinPlan pl = make_plan(cfg, 3, 2, tc, cfg->lengths);
   const LinLayout l = make_layout(cfg, pl, 2, false);
   if ((s = check_ws(cfg, l.total)) != VDN_OK) return s;
   if (cfg->tokens > 0 &&

@@ -26,6 +26,77 @@ __device__ __forceinline__ int lin_horizon(float log2_decay, int chunk) {
   return log2_decay < 0.f ? (int)fminf(160.f / -log2_decay / (float)chunk, 1e9f) + 2 : 1 << 30;
 }
 
+// Where the ranges of a split plan begin, and which of them hold a head's ends.  With lengths, a list cut into equal
+// parts would leave the CTAs of the padding without work: it is cut into parts of equal cost, a chunk without tokens (its
+// output rows are zeros, nothing is read) an eighth of one with tokens.  Every kernel of a call cuts by this rule.  Not for
+// batches above kLinCutBatch, nor where a part would be less than one chunk with tokens (two ranges
+// could begin at one).  Whole warps make and use it, with the same arguments in all lanes unless it says otherwise.
+class LinCuts {
+ public:
+  __device__ __forceinline__ LinCuts(const LinPlan& plan, const int* lengths, int B, int H, int N, int reverse)
+      : pl_(plan), H_(H), rev_(reverse), n_(0), cost_(0) {
+    if (!pl_.split || !lengths || B > kLinCutBatch) return;
+    const int lane = threadIdx.x & 31;
+    if (lane < B) n_ = (lin_length(lengths, lane, N) + pl_.chunk - 1) / pl_.chunk;
+    to_ = lane < B ? (long long)head_cost(n_) * H : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const long long v = __shfl_up_sync(0xffffffffu, to_, o);
+      if (lane >= o) to_ += v;
+    }
+    cost_ = __shfl_sync(0xffffffffu, to_, 31);
+    if (cost_ < (long long)kWhole * pl_.grid) cost_ = 0;
+  }
+  __device__ __forceinline__ long long start(int j) const {
+    if (cost_ == 0) return pl_.start(j);
+    if (j >= pl_.grid) return pl_.total;
+    const long long c = cost_ * j / pl_.grid;
+    const int b = __popc(__ballot_sync(0xffffffffu, to_ <= c)), n = __shfl_sync(0xffffffffu, n_, b), cost = head_cost(n);
+    const long long in = c - (__shfl_sync(0xffffffffu, to_, b) - (long long)cost * H_);
+    const int h = (int)(in / cost);
+    return ((long long)b * H_ + h) * pl_.nc + chunk_at((int)(in - (long long)h * cost), n);
+  }
+
+  // Head bh: the ranges that hold its first and its last chunk; chunk (of the head) at which range j, another one in each
+  // lane, begins, if it begins inside.
+  struct Head {
+    int first, last, n;
+    long long before;
+  };
+  __device__ __forceinline__ Head head(int bh) const {
+    Head r = {0, 0, 0, 0};
+    if (cost_ == 0) {
+      r.first = pl_.range_of((long long)bh * pl_.nc);
+      r.last = pl_.range_of((long long)bh * pl_.nc + pl_.nc - 1);
+      return r;
+    }
+    const int b = bh / H_;
+    r.n = __shfl_sync(0xffffffffu, n_, b);
+    r.before = __shfl_sync(0xffffffffu, to_, b) - (long long)head_cost(r.n) * (H_ - (bh - b * H_));
+    r.first = below(r.before + ((rev_ ? r.n == pl_.nc : r.n > 0) ? kWhole : 1));
+    r.last = below(r.before + head_cost(r.n));
+    return r;
+  }
+  __device__ __forceinline__ int start_in(const Head& a, int bh, int j) const {
+    const long long u = cost_ == 0 ? pl_.start(j) - (long long)bh * pl_.nc : cost_ * j / pl_.grid - a.before;
+    return u <= 0 ? 0 : cost_ == 0 ? (int)u : chunk_at((int)u, a.n);
+  }
+
+ private:
+  static constexpr int kWhole = 8;
+  __device__ __forceinline__ int head_cost(int n) const { return n * (kWhole - 1) + pl_.nc; }
+  // the chunk (walk order) at which r of a head's cost is spent, of a head with n chunks with tokens
+  __device__ __forceinline__ int chunk_at(int r, int n) const {
+    const int pad = pl_.nc - n;
+    return rev_ ? (r < pad ? r : pad + (r - pad) / kWhole) : r < n * kWhole ? r / kWhole : r - n * (kWhole - 1);
+  }
+  // the last range that begins before cost c
+  __device__ __forceinline__ int below(long long c) const { return (int)((c * pl_.grid + cost_ - 1) / cost_ - 1); }
+  const LinPlan& pl_;
+  int H_, rev_, n_;           // n_: chunks with tokens of the lane's sequence
+  long long to_ = 0, cost_;   // cost of the sequences up to the lane's, of all; 0: equal parts
+};
+
 // A stretch of one CTA's range inside one head: chunks [u0, u1) in walk order.
 struct LinPiece {
   int bh, u0, u1;
@@ -45,16 +116,14 @@ __device__ __forceinline__ void lin_real(int u0, int u1, int len, const LinPlan&
   if (a > b) a = b = u0;
 }
 
-// Range j's stretch (len: its head's tokens).
-__device__ __forceinline__ LinStretch lin_stretch(int j, int len, float log2_decay, const LinPlan& pl, int reverse) {
-  const long long t1 = pl.start(j + 1), head0 = (t1 - 1) / pl.nc * pl.nc, t0 = max(pl.start(j), head0);
+// The stretch of a range that has chunks [u0, u1) of its last head (len: that head's tokens).
+__device__ __forceinline__ LinStretch lin_stretch(int u0, int u1, int len, float log2_decay, const LinPlan& pl, int reverse) {
   LinStretch s;
-  s.bh = (int)(head0 / pl.nc);
-  if (t1 == head0 + pl.nc) {
+  if (u1 == pl.nc) {
     s.u0 = s.u1 = s.end = 0;
     return s;
   }
-  lin_real((int)(t0 - head0), (int)(t1 - head0), len, pl, reverse, s.u0, s.u1);
+  lin_real(u0, u1, len, pl, reverse, s.u0, s.u1);
   s.u0 = max(s.u0, s.u1 - lin_horizon(log2_decay, pl.chunk));
   s.end = s.u1;
   return s;

@@ -195,9 +195,12 @@ __global__ void __launch_bounds__(kThreads) lin_states_simt(const __grid_constan
   const LinWalk& wk = p.walk[blockIdx.y];
   pdl_release();
   const int range = blockIdx.x / pl.sub;
-  const int bh = (int)((pl.start(range + 1) - 1) / pl.nc), b = bh / p.H, h = bh % p.H, len = lin_length(p.lengths, b, p.N);
+  const LinCuts cuts(pl, p.lengths, p.B, p.H, p.N, wk.reverse);
+  const long long t0 = cuts.start(range), t1 = cuts.start(range + 1);
+  const int bh = (int)((t1 - 1) / pl.nc), b = bh / p.H, h = bh % p.H, len = lin_length(p.lengths, b, p.N);
+  const long long head0 = (long long)bh * pl.nc;
   const float l2 = lin_log2_decay(p.log_decay[h]);
-  const LinStretch st = lin_piece_of(lin_stretch(range, len, l2, pl, wk.reverse), blockIdx.x % pl.sub, pl);
+  const LinStretch st = lin_piece_of(lin_stretch((int)(max(t0, head0) - head0), (int)(t1 - head0), len, l2, pl, wk.reverse), blockIdx.x % pl.sub, pl);
   if (st.u0 == st.u1) return;
   StateTile<D> W;
   W.zero();
@@ -235,8 +238,9 @@ __global__ void __launch_bounds__(kThreads) lin_out_simt(const __grid_constant__
   // output tile of a thread: kR rows of four columns
   constexpr int kQuads = D / 4, kR = kC / (kThreads / kQuads);
   const int c = tid % kQuads * 4, r0 = tid / kQuads * kR;
-  long long t = pl.start(blockIdx.x);
-  const long long t_end = pl.start(blockIdx.x + 1);
+  const LinCuts cuts(pl, p.lengths, p.B, p.H, p.N, rev);
+  long long t = cuts.start(blockIdx.x);
+  const long long t_end = cuts.start(blockIdx.x + 1);
   pdl_wait();
   while (t < t_end) {
     const LinPiece pc(t, t_end, pl);
@@ -346,8 +350,9 @@ __global__ void __launch_bounds__(128) lin_scan(const __grid_constant__ LinState
   pdl_release();
   const int per = (DD + kE * (int)blockDim.x - 1) / (kE * (int)blockDim.x);  // blocks of a head
   const int bh = blockIdx.x / per, b = bh / p.H, h = bh % p.H, sub = pl.sub, lg = sub == 4 ? 2 : sub - 1;
-  const long long head0 = (long long)bh * pl.nc;
-  const int j0 = pl.range_of(head0), j1 = pl.range_of(head0 + pl.nc - 1);
+  const LinCuts cuts(pl, p.lengths, p.B, p.H, p.N, wk.reverse);
+  const LinCuts::Head head = cuts.head(bh);
+  const int j0 = head.first, j1 = head.last;
   if (j1 == j0) return;
   const int len = lin_length(p.lengths, b, p.N);
   const float l2 = lin_log2_decay(p.log_decay[h]);
@@ -357,10 +362,11 @@ __global__ void __launch_bounds__(128) lin_scan(const __grid_constant__ LinState
   const int n = (j1 - j0) * sub;
   for (int i = threadIdx.x; i < n; i += blockDim.x) {
     const int j = j0 + (i >> lg);
-    const LinStretch st = lin_piece_of(lin_stretch(j, len, l2, pl, wk.reverse), i & (sub - 1), pl);
+    const int u0 = cuts.start_in(head, bh, j), u1 = cuts.start_in(head, bh, j + 1);
+    const LinStretch st = lin_piece_of(lin_stretch(u0, u1, len, l2, pl, wk.reverse), i & (sub - 1), pl);
     has[i] = st.u0 < st.u1;
     if ((i & (sub - 1)) == 0)
-      fall[i >> lg] = lin_pow(l2, lin_rows((int)(max(pl.start(j), head0) - head0), (int)(pl.start(j + 1) - head0), len, pl, wk.reverse));
+      fall[i >> lg] = lin_pow(l2, lin_rows(u0, u1, len, pl, wk.reverse));
   }
   __syncthreads();
   pdl_wait();

@@ -66,7 +66,8 @@ struct TcLayout {
   static constexpr int kTab = kZero + (D == 64 ? 2048 : 0);  // lambda^0..31 of a piece's head between zeros, two in turn
   static constexpr int kStage = D == 128 ? kW : kTab + 1024;  // its rows on their way out: W's tile (see there), or 8 x 2 KB
   static constexpr int kBar = D == 128 ? kTab + 2 * 384 : kStage + 8 * 2048;
-  static constexpr int kBytes = kBar + 288 + 1024;
+  static constexpr int kRange = kBar + 288;  // the CTA's range: its first chunk and the next range's
+  static constexpr int kBytes = kRange + 16 + 1024;
 };
 static_assert(TcLayout<128>::kBytes <= 232448 && TcLayout<64>::kBytes <= 232448, "shared memory of an SM");
 
@@ -300,7 +301,9 @@ __device__ __forceinline__ bool third_part(float l2, int rows) { return l2 != 0.
 
 }  // namespace
 
-template <int D>
+// kSplit: of a plan with equal parts.  Whole heads have a kernel of their own: the ranges' ends come from the parameters
+// there, and with them in other registers the 64-column walk took 6 % longer (gradients at 8 x 8000 x 4 x 64: 177 us and 166).
+template <int D, bool kSplit>
 __global__ void __launch_bounds__(kTcThreads, 1) lin_out_tc(const __grid_constant__ LinTcMaps maps,
                                                             const __grid_constant__ LinOutParams p) {
   using L = TcLayout<D>;
@@ -313,7 +316,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lin_out_tc(const __grid_constan
   const LinPlan& pl = p.pl;
   const LinJob& jb = p.job[blockIdx.x % p.n_jobs];
   const int range = blockIdx.x / p.n_jobs, rev = jb.reverse;
-  const long long t_begin = pl.start(range), t_end = pl.start(range + 1);
+  long long* range_at = reinterpret_cast<long long*>(smem + L::kRange);
   const uint32_t warp = warp_id(), lane = lane_id();
 
   if (threadIdx.x == 0) {
@@ -334,6 +337,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) lin_out_tc(const __grid_constan
     ab->given_up = 0;
     fence_mbar_init();
   }
+  if (kSplit && warp == 2) {
+    const LinCuts cuts(pl, p.lengths, p.B, p.H, p.N, rev);
+    const long long t0 = cuts.start(range), t1 = cuts.start(range + 1);
+    if (lane == 0) range_at[0] = t0, range_at[1] = t1;
+  }
   if (D == 64)
     for (int i = threadIdx.x; i < 2048 / 16; i += kTcThreads)
       reinterpret_cast<uint4*>(smem + L::kZero)[i] = make_uint4(0, 0, 0, 0);
@@ -346,6 +354,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) lin_out_tc(const __grid_constan
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // (uniform registers)
+  const long long t_begin = kSplit ? __shfl_sync(0xffffffffu, range_at[0], 0) : pl.start(range),
+                  t_end = kSplit ? __shfl_sync(0xffffffffu, range_at[1], 0) : pl.start(range + 1);
 
   if (warp < 4) {
     regs_dec<kCtlRegs>();
@@ -614,14 +625,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) lin_out_tc(const __grid_constan
       int ua, ub;
       lin_real(pc.u0, pc.u1, len, pl, rev, ua, ub);
       const float l2 = lin_log2_decay(p.log_decay[h]);
-      __nv_bfloat16* o = out_base + b * jb.o.sb + h * jb.o.sh + z0;
+      __nv_bfloat16* o = out_base + b * jb.o.sb + h * jb.o.sh;
       // chunks behind the sequence
+#pragma unroll 1
       for (int u = pc.u0; u < pc.u1; ++u) {
-        const int row0 = (rev ? pl.nc - 1 - u : u) * kChunk;
-        if (row0 < len || row0 + r >= p.N || z0 >= d) continue;
-#pragma unroll
-        for (int e = 0; e < kCols; e += 8)
-          *reinterpret_cast<uint4*>(o + (long long)(row0 + r) * jb.o.sn + e) = make_uint4(0, 0, 0, 0);
+        const int row0 = (rev ? pl.nc - 1 - u : u) * kChunk, lg = D == 128 ? 4 : d == 64 ? 3 : 2;  // 2^lg units in a row
+        const int units = min(kChunk, p.N - row0) << lg;
+        if (row0 < len) continue;
+#pragma unroll 1
+        for (int i = threadIdx.x - 128 - kDecay; i < units; i += kOut)
+          *reinterpret_cast<uint4*>(o + (long long)(row0 + (i >> lg)) * jb.o.sn + (i & ((1 << lg) - 1)) * 8) =
+              make_uint4(0, 0, 0, 0);
       }
       // the state before the piece
       if (!waited) pdl_wait();
@@ -747,6 +761,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) lin_out_tc(const __grid_constan
 
 namespace {
 
+constexpr int kStMost = kLinMaxSub;  // pieces of a CTA: those of kLinSms ranges, shared by as many CTAs
+
 template <int D>
 struct StLayout {
   static constexpr int kTile = kChunk * D * 2;
@@ -758,7 +774,8 @@ struct StLayout {
   }
   static constexpr int kZero = kLo + 2 * kTile;
   static constexpr int kBar = kZero + (D == 64 ? 2048 : 0);
-  static constexpr int kBytes = kBar + 288 + 1024;
+  static constexpr int kPieces = kBar + 288;  // the CTA's pieces
+  static constexpr int kBytes = kPieces + kStMost * 48 + 1024;
 };
 static_assert(StLayout<128>::kBytes <= 232448 && StLayout<64>::kBytes <= 232448, "shared memory of an SM");
 enum { sFull = 0, sEmpty = 8, sReady = 16, sLoFree = 18, sAccFull = 20, sAccFree = 22, sDone = 24, sNumBars };
@@ -768,23 +785,28 @@ constexpr int kStThreads = 64 + kStWorkers + 128;
 
 // One of the pieces that a CTA of the ranges' states goes through.
 struct StPiece {
-  int range, h, b, len, rev, u0, u1, end;
-  float l2;
   const LinWalk* wk;
+  int slot, h, b, len, rev, u0, u1, end;  // slot: its place among the walk's parts
+  float l2;
   __device__ __forceinline__ StPiece(int i, const LinStateParams& p) {
     const LinPlan& pl = p.pl;
     wk = &p.walk[i % p.n_walks];
-    i /= p.n_walks;
-    range = i / pl.sub;
+    slot = i / p.n_walks;
+    const int range = slot / pl.sub;
     rev = wk->reverse;
-    const int bh = (int)((pl.start(range + 1) - 1) / pl.nc);
+    const LinCuts cuts(pl, p.lengths, p.B, p.H, p.N, rev);
+    const long long t0 = cuts.start(range), t1 = cuts.start(range + 1);
+    const int bh = (int)((t1 - 1) / pl.nc);
     b = bh / p.H, h = bh % p.H;
     len = lin_length(p.lengths, b, p.N);
     l2 = lin_log2_decay(p.log_decay[h]);
-    const LinStretch st = lin_piece_of(lin_stretch(range, len, l2, pl, rev), i % pl.sub, pl);
+    const long long head0 = (long long)bh * pl.nc;
+    const LinStretch st =
+        lin_piece_of(lin_stretch((int)(max(t0, head0) - head0), (int)(t1 - head0), len, l2, pl, rev), slot % pl.sub, pl);
     u0 = st.u0, u1 = st.u1, end = st.end;
   }
 };
+static_assert(sizeof(StPiece) == 48, "room in shared memory");
 
 }  // namespace
 
@@ -803,7 +825,9 @@ __global__ void __launch_bounds__(kStThreads, 1) lin_states_tc(const __grid_cons
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kBar + sNumBars * 8);
   WaitRecord* ab = reinterpret_cast<WaitRecord*>(smem + L::kBar + sNumBars * 8 + 8);
   const LinPlan& pl = p.pl;
-  const int n_pieces = p.n_walks * pl.grid * pl.sub;
+  // the CTA's pieces, gridDim apart
+  StPiece* pieces = reinterpret_cast<StPiece*>(smem + L::kPieces);
+  const int n_pieces = (p.n_walks * pl.grid * pl.sub - blockIdx.x + gridDim.x - 1) / gridDim.x;
   pdl_release();
   const uint32_t warp = warp_id(), lane = lane_id();
 
@@ -822,6 +846,11 @@ __global__ void __launch_bounds__(kStThreads, 1) lin_states_tc(const __grid_cons
     ab->given_up = 0;
     fence_mbar_init();
   }
+  if (warp == 2)
+    for (int k = 0; k < n_pieces; ++k) {
+      const StPiece pc(blockIdx.x + k * gridDim.x, p);
+      if (lane == 0) pieces[k] = pc;
+    }
   if (D == 64)
     for (int i = threadIdx.x; i < 2048 / 16; i += kStThreads)
       reinterpret_cast<uint4*>(smem + L::kZero)[i] = make_uint4(0, 0, 0, 0);
@@ -839,8 +868,8 @@ __global__ void __launch_bounds__(kStThreads, 1) lin_states_tc(const __grid_cons
     if (lane == 0) {
       int i = 0;
       bool ok = true;
-      for (int k = blockIdx.x; k < n_pieces && ok; k += gridDim.x) {
-        const StPiece pc(k, p);
+      for (int k = 0; k < n_pieces && ok; ++k) {
+        const StPiece& pc = pieces[k];
         if (pc.u0 == pc.u1) continue;
         const MapRef my(maps.m[pc.wk->my]), mz(maps.m[pc.wk->mz]);
         for (int u = pc.u0; u < pc.u1 && ok; ++u) {
@@ -869,8 +898,8 @@ __global__ void __launch_bounds__(kStThreads, 1) lin_states_tc(const __grid_cons
     };
     bool ok = true;
     int c = 0, done = 0;  // chunks; pieces
-    for (int k = blockIdx.x; k < n_pieces && ok; k += gridDim.x) {
-      const StPiece pc(k, p);
+    for (int k = 0; k < n_pieces && ok; ++k) {
+      const StPiece& pc = pieces[k];
       if (pc.u0 == pc.u1) continue;
       const int buf = done & 1;
       if (done > 1 && !(ok = wait(&bars[sAccFree + buf], ((done >> 1) & 1) ^ 1))) break;
@@ -902,8 +931,8 @@ __global__ void __launch_bounds__(kStThreads, 1) lin_states_tc(const __grid_cons
     bool ok = true;
     int c = 0;
     bool both = false;  // the chunk before takes both tiles of parts
-    for (int k = blockIdx.x; k < n_pieces && ok; k += gridDim.x) {
-      const StPiece pc(k, p);
+    for (int k = 0; k < n_pieces && ok; ++k) {
+      const StPiece& pc = pieces[k];
       for (int u = pc.u0; u < pc.u1; ++u, ++c) {
         const int row0 = (pc.rev ? pl.nc - 1 - u : u) * kChunk, n = min(pc.len - row0, kChunk);
         const int ty = 2 * c, tz = ty + 1, more = lin_rows(u + 1, pc.end, pc.len, pl, pc.rev);
@@ -931,13 +960,13 @@ __global__ void __launch_bounds__(kStThreads, 1) lin_states_tc(const __grid_cons
     // read-out of finished pieces: a thread has a row
     const int q = warp & 3, r = q * 32 + lane, d = D == 128 ? 128 : p.d;
     int done = 0;
-    for (int k = blockIdx.x; k < n_pieces; k += gridDim.x) {
-      const StPiece pc(k, p);
+    for (int k = 0; k < n_pieces; ++k) {
+      const StPiece& pc = pieces[k];
       if (pc.u0 == pc.u1) continue;
       const int buf = done & 1;
       if (__any_sync(0xffffffffu, !lin_wait(&bars[sAccFull + buf], (done >> 1) & 1, ab))) break;
       tc_fence_after();
-      float* dst = pc.wk->parts + (long long)(k / p.n_walks) * d * d + (long long)r * d;
+      float* dst = pc.wk->parts + (long long)pc.slot * d * d + (long long)r * d;
 #pragma unroll 1
       for (int e = 0; e < D; e += 16) {
         uint32_t x[16];
@@ -967,14 +996,14 @@ __global__ void __launch_bounds__(kStThreads, 1) lin_states_tc(const __grid_cons
 
 namespace {
 
-template <int D>
+template <int D, bool kSplit>
 cudaError_t out_tc(const LinTcMaps& m, const LinOutParams& p, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
   // the warps' register shares are drawn from what the CTA was launched with
-  const cudaError_t e = lin_prepare((const void*)lin_out_tc<D>, TcLayout<D>::kBytes, kTcRegs, done);
+  const cudaError_t e = lin_prepare((const void*)lin_out_tc<D, kSplit>, TcLayout<D>::kBytes, kTcRegs, done);
   if (e != cudaSuccess) return e;
-  if (p.pl.split) return launch_after(lin_out_tc<D>, p.n_jobs * p.pl.grid, kTcThreads, TcLayout<D>::kBytes, st, m, p);
-  lin_out_tc<D><<<p.n_jobs * p.pl.grid, kTcThreads, TcLayout<D>::kBytes, st>>>(m, p);
+  if (kSplit) return launch_after(lin_out_tc<D, kSplit>, p.n_jobs * p.pl.grid, kTcThreads, TcLayout<D>::kBytes, st, m, p);
+  lin_out_tc<D, kSplit><<<p.n_jobs * p.pl.grid, kTcThreads, TcLayout<D>::kBytes, st>>>(m, p);
   return cudaGetLastError();
 }
 
@@ -983,7 +1012,9 @@ cudaError_t states_tc(const LinTcMaps& m, const LinStateParams& p, cudaStream_t 
   static std::atomic<unsigned long long> done{0};
   const cudaError_t e = lin_prepare((const void*)lin_states_tc<D>, StLayout<D>::kBytes, 0, done);
   if (e != cudaSuccess) return e;
-  lin_states_tc<D><<<std::min(kLinSms, p.n_walks * p.pl.grid * p.pl.sub), kStThreads, StLayout<D>::kBytes, st>>>(m, p);
+  const int pieces = p.n_walks * p.pl.grid * p.pl.sub;
+  if (pieces > kStMost * kLinSms) return cudaErrorInvalidValue;  // no plan has more
+  lin_states_tc<D><<<std::min(kLinSms, pieces), kStThreads, StLayout<D>::kBytes, st>>>(m, p);
   return cudaGetLastError();
 }
 
@@ -1004,7 +1035,8 @@ cudaError_t lin_prepare(const void* kernel, int smem_bytes, int min_regs, std::a
 }
 
 cudaError_t launch_lin_out_tc(const LinTcMaps& m, const LinOutParams& p, cudaStream_t st) {
-  return p.d == 128 ? out_tc<128>(m, p, st) : out_tc<64>(m, p, st);
+  if (p.pl.split) return p.d == 128 ? out_tc<128, true>(m, p, st) : out_tc<64, true>(m, p, st);
+  return p.d == 128 ? out_tc<128, false>(m, p, st) : out_tc<64, false>(m, p, st);
 }
 
 cudaError_t launch_lin_states_tc(const LinTcMaps& m, const LinStateParams& p, cudaStream_t st) {

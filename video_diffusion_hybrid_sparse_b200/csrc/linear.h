@@ -36,6 +36,7 @@ namespace vdn {
 constexpr int kLinSms = 148;          // CTAs a wave holds (one for each SM of a B200)
 constexpr int kLinMaxGrid = 2 * kLinSms;  // most ranges of a split plan
 constexpr int kLinMaxSub = 4;             // most pieces of a range's part
+constexpr int kLinCutBatch = 32;          // most sequences that ranges are cut by the lengths of (LinCuts): a warp's lanes
 constexpr int kLinSimtChunk = 64;     // rows of a chunk: fp32 kernels
 constexpr int kLinTcChunk = 128;      // rows of a chunk: tensor-core kernels
 
@@ -55,7 +56,8 @@ struct LinTcMaps {
 
 // The chunks of every (batch, head), (batch, head)-major and in walk order,
 // form one list; CTA j takes [start(j), start(j + 1)): whole heads, as many as
-// make one wave of CTAs, or equal parts.  Where a range begins
+// make one wave of CTAs, or equal parts (by cost where sequences have lengths:
+// LinCuts).  Where a range begins
 // inside a head, the state before it is the sum of what the earlier ranges of
 // that head leave: each range's own share ("part") is formed by a first kernel,
 // a scan over the ranges adds them up, and the walk starts from the result.
@@ -82,7 +84,7 @@ VDN_HD int lin_rows(int u0, int u1, int n, const LinPlan& pl, int reverse) {
 // The chunks that carry the part of range j (walk order): the range's last stretch, if its head goes on behind it, from
 // where a token's decay to the stretch's end is not 0 in fp32; piece i of it.  Empty: u0 == u1.
 struct LinStretch {
-  int bh, u0, u1, end;
+  int u0, u1, end;
 };
 
 struct LinJob {
