@@ -372,6 +372,31 @@ def test_streams_graphs_and_repeats(dtype, N, d):
         assert all(torch.equal(a, b) for a, b in zip(o, w))
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+def test_captured_call_with_new_lengths(dtype):
+    """A captured call follows the lengths that its tensor holds at the replay."""
+    B, N, H, d = 4, 3000, 3, 64
+    q, k, v, do = tensors(B, N, H, d, dtype, names="qkvo")
+    ld, s0 = decays(H), states(B, H, d, 5)
+    lengths = torch.tensor([N, N, N, N], dtype=torch.int32, device="cuda")
+
+    def call(n):
+        last, din = torch.empty_like(s0), torch.empty_like(s0)
+        out = vb.linear_attn_fwd(q, k, v, ld, state_in=s0, state_out=last, lengths=n)
+        return (out, last, din) + vb.linear_attn_bwd(q, k, v, ld, do, state_in=s0, d_state_out=last, d_state_in=din, lengths=n)
+
+    call(lengths)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = call(lengths)
+    for new in ([N, 0, 5, 2000], [0, 0, 0, 0], [100, 100, 100, 2999], [N, N, N, N]):
+        lengths.copy_(torch.tensor(new, dtype=torch.int32))
+        want = call(lengths.clone())
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_no_tokens():
     B, H, d = 2, 2, 64
     q = torch.empty(B, 0, H, d, device="cuda", dtype=BF16)
