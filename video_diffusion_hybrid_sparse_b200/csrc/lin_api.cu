@@ -93,10 +93,16 @@ bool on_tensor_cores(const vdn_linear_cfg* c, std::initializer_list<const vdn_vi
   return true;
 }
 
-// Ranges: whole heads, or equal parts of all heads' chunks, which cost a kernel for the parts' states (`walks` of them,
-// half of a job's work each) and the scan.  In chunks of one CTA; the two kernels' launches, and the scan, are worth some
-// (`launches`, from sweeps of 1 to 300 heads of 100 to 4000 tokens: with 8 for all, a call of 8 heads took 66 us instead of
-// 28 at 400 fp32 tokens and 26.9 instead of 17.6 at 1000 bf16 ones; with 4 and 1, 64 heads take 1.2-1.4 times as long).
+// Ranges: whole heads, or equal parts of all heads' chunks, which cost a kernel for the parts' states (half of a job's work,
+// for `walks` states), the scan and two launches.  Which is shorter, in chunks of a CTA:
+//
+// bf16: parts as if states were formed over all chunks, and 5 (6 at head_dim 128) for scan and launches (with 8, eight heads
+// of 1000 tokens took 26.9 us instead of 17.6; with 4, 64 heads of 2048 took 56.8 instead of 45.8).
+// fp32: states are formed over the stretches of ranges that end inside a head only, which is counted (20 x 2000 x 15 x 128:
+// 1621 us in parts, 2092 in heads; the bf16 kernels, bound by memory and latency, took 1.05-1.25 times as long for
+// 150 to 400 heads with it).  Where two CTAs share an SM, a chunk of one alone takes 0.65 to 0.75 of the time (9.5 us and
+// 15 at head_dim 64).
+//
 // Sequences of a padded batch are taken to fill three quarters of it, which parts make use of (LinCuts) and whole heads do
 // not: gradients at 4 x 3840 x 16 x 128 take 213 us in whole heads whatever the lengths, in parts 128 to 228 us.
 LinPlan make_plan(const vdn_linear_cfg* c, int jobs, int walks, bool tc, bool padded) {
@@ -107,11 +113,18 @@ LinPlan make_plan(const vdn_linear_cfg* c, int jobs, int walks, bool tc, bool pa
   pl.total = heads * pl.nc;
   const int per_wave = tc ? kLinSms : lin_simt_ctas(c->head_dim);
   const int most = per_wave / jobs;
-  const long long whole = (heads + most - 1) / most * pl.nc;
-  const int launches = !tc ? 2 : c->head_dim == 128 ? 6 : 5;
   const long long work = padded && c->batch <= kLinCutBatch ? pl.total - pl.total / 4 : pl.total;
-  const long long parts = (work * (2 * jobs + walks) + 2 * per_wave - 1) / (2 * per_wave) + launches;
-  pl.split = parts < whole;
+  if (tc) {
+    const long long whole = (heads + most - 1) / most * pl.nc;
+    pl.split = (work * (2 * jobs + walks) + 2 * per_wave - 1) / (2 * per_wave) + (c->head_dim == 128 ? 6 : 5) < whole;
+  } else {
+    const double alone = per_wave == kLinSms ? 1.0 : c->head_dim == 64 ? 0.65 : 0.75;
+    auto pace = [&](long long ctas) { return ctas * jobs <= kLinSms ? alone : 1.0; };
+    const double nc = pl.nc, range = (double)((work + most - 1) / most);
+    const double whole = nc * ((heads - 1) / most + pace((heads - 1) % most + 1));
+    const double stretch = range < nc ? range * (1.0 - range / (2.0 * nc)) : 0.5 * nc;
+    pl.split = (range + 0.5 * walks / jobs * stretch) * pace(std::min<long long>(most, pl.total)) + 1.6 < whole;
+  }
   pl.grid = (int)std::min<long long>(most, pl.split ? pl.total : heads);
   // a range's part in one, two or four pieces, of eight chunks at least
   const long long eights = pl.split ? pl.total / pl.grid / 8 : 1;
