@@ -21,6 +21,7 @@
 #include <type_traits>
 
 #include "norm.h"
+#include "norm_range.h"
 #include "pdl.cuh"
 #include "sm100.cuh"
 
@@ -229,22 +230,17 @@ __device__ __forceinline__ uint32_t most_bits(const Pairs& f, int a, int b, uint
   return m;
 }
 
-constexpr float kBigDown = 0x1p-64f, kSmallUp = 0x1p64f;
-
-// Factor that brings a row's elements back where 32 bits hold their squares: 1
-// unless the sum of squares has overflowed, or vanishes and eps does not cover it.
-__device__ __forceinline__ float rescue(float sum, float eps) {
-  if (!(sum < INFINITY)) return kBigDown;
-  return sum < 0x1p-80f && eps < 0x1p-80f ? kSmallUp : 1.f;
-}
-
 // 1 / rms of the row whose G threads hold h, where the elements may have been
 // multiplied by `mul` (a power of two) on return: mul / rms belongs to them.
-// The second look at the registers is a choice of the whole block (it has a
-// barrier), which each thread reads from all warps' sums.
+// The second look at the registers is a choice of the whole block (it has
+// barriers), made of the sums of its real rows: `left` rows are left from the
+// block's first on, and this row exists if `real` (one that does not is zeros,
+// and is normed with eps 1: eps may be 0).
 template <int G, int kV>
-__device__ __forceinline__ float row_rstd(Pairs (&h)[kV], int W, float eps, float* slot, float& mul) {
+__device__ __forceinline__ float row_rstd(Pairs (&h)[kV], int W, float eps, bool real, long long left, float* slot,
+                                          float& mul) {
   mul = 1.f;
+  const float own_eps = real ? eps : 1.f;
   auto squares = [&] {
     uint64_t s = 0;
 #pragma unroll
@@ -256,20 +252,15 @@ __device__ __forceinline__ float row_rstd(Pairs (&h)[kV], int W, float eps, floa
     return a + b;
   };
   float sum = row_reduce<G, false>(squares(), slot);
-  bool again = rescue(sum, eps) != 1.f;
+  const float own = norm_rescue(sum, own_eps);
+  bool again = own != 1.f;
   if constexpr (G > 32 && G < 256) {
-    constexpr int kWarps = G / 32, kRows = block_of(G) / G;
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      float s = slot[r * kWarps];
-#pragma unroll
-      for (int i = 1; i < kWarps; ++i) s += slot[r * kWarps + i];
-      again |= rescue(s, eps) != 1.f;
-    }
+    constexpr int kRows = block_of(G) / G;
+    again = norm_look_again<kRows, G / 32>(slot, left < kRows ? (int)left : kRows, eps);
   }
   if constexpr (G < 32) again = __any_sync(0xffffffffu, again);  // the warp's rows share shuffles
   if (again) {
-    mul = rescue(sum, eps);
+    mul = own;
     const uint64_t m2 = f32x2_pack(mul, mul);
 #pragma unroll
     for (int i = 0; i < kV; ++i)
@@ -278,7 +269,7 @@ __device__ __forceinline__ float row_rstd(Pairs (&h)[kV], int W, float eps, floa
     if constexpr (G > 32) __syncthreads();  // the first sums have been read
     sum = row_reduce<G, false>(squares(), slot);
   }
-  return rsqrtf(sum / (float)W + eps * mul * mul);
+  return rsqrtf(sum / (float)W + own_eps * mul * mul);
 }
 
 }  // namespace
@@ -328,7 +319,7 @@ __global__ void __launch_bounds__(block_of(G), blocks_of<T, kVec>(G)) norm_fwd(c
       for (int i = 0; i < kV; ++i) store_pairs<T, G, kVec>(ro, h[i], C::first(i, t), p.W);
     }
     float mul;
-    const float rstd = row_rstd<G, kV>(h, p.W, real ? p.eps : 1.f, s_sum[par], mul);
+    const float rstd = row_rstd<G, kV>(h, p.W, p.eps, real, p.rows - first, s_sum[par], mul);
     const uint64_t rstd2 = f32x2_pack(rstd, rstd);
 #pragma unroll
     for (int i = 0; i < kV; ++i) {
@@ -421,7 +412,7 @@ __global__ void __launch_bounds__(1024) norm_fwd_wide(const __grid_constant__ No
     return row_reduce<G, false>(sum, s_sum);
   };
   float sum = squares();
-  if ((mul = rescue(sum, p.eps)) != 1.f) {
+  if ((mul = norm_rescue(sum, p.eps)) != 1.f) {
     __syncthreads();
     sum = squares();
   }
@@ -515,8 +506,7 @@ __global__ void __launch_bounds__(block_of(G), G <= 256 ? 2 : 1) norm_bwd(const 
     }
     if constexpr (kAhead) fetch(row + step);
     float mul;
-    // h * rn is the normed row; a row that does not exist is zeros (eps may be 0)
-    const float rn = row_rstd<G, kV>(h, p.W, real ? p.eps : 1.f, s_sq, mul);
+    const float rn = row_rstd<G, kV>(h, p.W, p.eps, real, p.rows - first, s_sq, mul);  // h * rn is the normed row
     const uint64_t rn2 = f32x2_pack(rn, rn);
     uint64_t gh = 0;
 #pragma unroll
@@ -577,7 +567,7 @@ __global__ void __launch_bounds__(block_of(G), G <= 256 ? 2 : 1) norm_bwd(const 
 }
 
 // Backward of rows of more than 32768 elements: a block a row, read twice; the
-// weight's gradient by norm_dweight_wide from each row's factors (rescue's and 1 / rms).
+// weight's gradient by norm_dweight_wide from each row's factors (norm_rescue's and 1 / rms).
 template <typename T>
 __global__ void __launch_bounds__(1024) norm_bwd_wide(const __grid_constant__ NormBwdParams p, float2* rstds) {
   constexpr int G = 1024;
@@ -602,7 +592,7 @@ __global__ void __launch_bounds__(1024) norm_bwd_wide(const __grid_constant__ No
     gh = row_reduce<G, false>(gh, s_gh);
   };
   sums();
-  if ((mul = rescue(sq, p.eps)) != 1.f) {
+  if ((mul = norm_rescue(sq, p.eps)) != 1.f) {
     __syncthreads();
     sums();
   }
