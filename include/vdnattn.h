@@ -432,8 +432,9 @@ VDN_API vdn_status vdn_linear_attn_step(const vdn_view* q, const vdn_view* k, co
  * values are rounded to nearest even.  A row that holds a NaN or an infinity
  * gives what the formula gives: NaN values and, under a scale, a NaN scale
  * where a NaN is in its reach.  Squares beyond fp32's range (elements above
- * 1e17, or, with eps = 0, below 1e-17) are summed of the row multiplied by a
- * power of two.
+ * 1e16, or, with eps below 2^-80, below 1e-12) are summed of the row multiplied
+ * by a power of two, so that every finite row is normed.  The gradients' 1 / rms
+ * itself is fp32: it overflows for rows of denormal numbers.
  *
  * Backward (of the tensor output; h is the stored residual_out, or x): with
  * g = dy * weight, r = 1 / sqrt(mean(h^2) + eps):

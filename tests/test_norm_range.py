@@ -46,6 +46,20 @@ def test_missing_rows_do_not_enter_the_choice(host):
         assert again == any(own[eps, repr(s)] for s in sums[:real]), (real, eps, sums)
 
 
+@pytest.mark.parametrize("W", [1, 2, 64, 2048, 16384, 32768, 40000, 1 << 20])
+def test_factors_bring_every_row_into_range(host, W):
+    """Rows of W equal elements from the smallest number to the largest, and of one such element among zeros: the squares'
+    sum, of the row times its factor, is a normal number."""
+    a = np.concatenate([np.float32(2.0) ** np.arange(-149, 128, dtype=np.float32), [np.finfo(np.float32).max]]).astype(np.float32)
+    with np.errstate(over="ignore", under="ignore"):
+        for n in (W, 1):
+            sums = a * a * np.float32(n)
+            f = np.array([x for _, x in host([(1, 0.0, s, 1, 1, 1) for s in sums])], dtype=np.float32)
+            scaled = a * f
+            again = scaled * scaled * np.float32(n)
+            assert np.isfinite(again).all() and (again >= np.finfo(np.float32).tiny).all(), a[~np.isfinite(again)]
+
+
 def normed(x, gamma, dy):
     """y, dx, dgamma with eps = 0, and the magnitudes of the last two, in 64 bits."""
     X, G, DY = x.double(), gamma.double(), dy.double()
@@ -92,3 +106,34 @@ def test_blocks_that_are_not_full(n, W, dtype):
     x[n // 2] *= 1e-25
     x[-1] *= 1e20
     check_rows(x, gamma, dy)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("W", [1, 2, 48, 100, 500, 520, 1000, 2048, 4096, 16384, 32768, 40000])
+def test_rows_at_the_ends_of_the_range(W, dtype):
+    """Rows whose elements are near the type's largest number or among its smallest (denormal ones forward only, where
+    1 / rms has no fp32)."""
+    x, dy = rows_of(7, W, dtype, 1), rows_of(7, W, dtype, 2)
+    gamma = 1.0 + 0.2 * rows_of(1, W, torch.float32, 3)[0]
+    sign = torch.where(x > 0, 1.0, -1.0)
+    some = 0.5 + 0.5 * x.float().abs().clamp(max=1.0)
+    for i, size in ((0, 3.3e38), (2, 1e38), (3, 1e37), (5, 2e-37)):
+        x[i] = (sign[i] * some[i] * size).to(dtype)
+    err, half = (W / 2 + 12) * 2.0 ** -24, HALF[dtype]
+    y, dx, size, dw, dw_size = normed(x, gamma, dy)
+    out = vb.add_rmsnorm_fwd(x, gamma, eps=0.0)
+    assert ((out.double() - y).abs() <= y.abs() * (err + half * 1.001)).all()
+    got, got_w = vb.add_rmsnorm_bwd(x, gamma, dy, eps=0.0)
+    # dx of the largest rows, and their 1 / rms, are denormal: half a step of 2^-149 (of the type) each
+    steps = 2.0 ** -150 * (1 + size * x.double().square().mean(1, keepdim=True).sqrt()) + (2.0 ** -134 if half else 0)
+    assert ((got.double() - dx).abs() <= size * (1.5 * W + 16) * 2.0 ** -24 + dx.abs() * half * 1.001 + steps).all()
+    assert ((got_w.double() - dw).abs() <= dw_size * (7 + W + 16) * 2.0 ** -24).all()
+    x[1], x[6] = (sign[1] * some[1] * 1e-39).to(dtype), 2.0 ** -133  # bf16's smallest number
+    y = normed(x, gamma, dy)[0]
+    out = vb.add_rmsnorm_fwd(x, gamma, eps=0.0)
+    assert ((out.double() - y).abs() <= y.abs() * (err + half * 1.001)).all()
+    for mode, group in ((vb.NORM_OUT_E4M3_ROW, W), (vb.NORM_OUT_E4M3_GROUP, 128)):
+        values, scales = vb.add_rmsnorm_fwd(x, gamma, eps=0.0, out_mode=mode)
+        s = scales.double().repeat_interleave(group, 1)[:, :W]
+        assert ((values.float().double() - y / s).abs() <= (y / s).abs() * (2.0 ** -4 + 3 * err) + 2.0 ** -10).all()

@@ -7,7 +7,10 @@
 
 namespace vdn {
 
-constexpr float kBigDown = 0x1p-64f, kSmallUp = 0x1p64f;
+// Any row of up to 2^20 finite elements, not all zero, is brought into range: a sum that overflows has an element of 2^54
+// or more, and 2^20 elements below 2^128 come to 2^116 after 2^-80; a sum below 2^-80 has elements below 2^-40 (2^112
+// after 2^96), the smallest of which, 2^-149, has a square of 2^-106.
+constexpr float kBigDown = 0x1p-80f, kSmallUp = 0x1p96f;
 
 // Factor that brings a row's elements back where 32 bits hold their squares: 1
 // unless the sum of squares has overflowed, or vanishes and eps does not cover it.
