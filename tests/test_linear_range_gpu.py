@@ -1,0 +1,41 @@
+"""The causal linear memory at the ends of its decays' range."""
+import pytest
+import torch
+
+import linear_reference as R
+from video_diffusion_hybrid_sparse_b200 import binding as vb
+
+pytestmark = pytest.mark.gpu
+BF16, FP32 = torch.bfloat16, torch.float32
+
+
+def tensors(B, N, H, d, dtype, seed):
+    g = torch.Generator("cuda").manual_seed(1000 * seed + 7 * N + d)
+    return [torch.randn(B, N, H, d, device="cuda", generator=g).to(dtype) for _ in range(4)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("N,lengths,log_decay", [
+    (1, None, (1.0, 0.5)), (10, None, (1.0, 2.0)), (40, None, (1.0, 0.7)), (127, None, (0.6, 0.1)),
+    (300, [10, 0, 25], (1.0, 0.9)), (300, [300, 129, 1], (0.2, 0.01)), (3000, [3000, 2050, 40], (0.02, -0.01)),
+])
+def test_growing_memory_of_short_sequences(N, lengths, log_decay, d, dtype):
+    """Decays above 1 whose power over a whole chunk has no fp32, in sequences that end before: all results are finite, those
+    of the formula."""
+    B, H = 3, 2
+    ld = torch.tensor(log_decay, device="cuda")
+    n = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    q, k, v, do = tensors(B, N, H, d, dtype, 1)
+    g = torch.Generator("cuda").manual_seed(5)
+    s0, ds = (torch.randn(B, H, d, d, device="cuda", generator=g) for _ in range(2))
+    for init, dlast in ((None, None), (s0, ds)):
+        ref = R.forward(q, k, v, ld, d ** -0.5, init, n)
+        state, din = torch.empty_like(s0), torch.empty_like(s0)
+        out = vb.linear_attn_fwd(q, k, v, ld, state_in=init, state_out=state, lengths=n)
+        R.check(out, ref["out"], "out", dtype, d, N)
+        R.check(state, ref["state"], "state", dtype, d, N)
+        ref = R.backward(q, k, v, ld, d ** -0.5, do, init, dlast, n)
+        grads = vb.linear_attn_bwd(q, k, v, ld, do, state_in=init, d_state_out=dlast, d_state_in=din, lengths=n)
+        for name, got in zip(("dq", "dk", "dv", "d_state_in"), (*grads, din)):
+            R.check(got, ref[name], name, dtype, d, N)

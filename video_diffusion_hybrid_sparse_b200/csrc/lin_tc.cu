@@ -189,9 +189,10 @@ __device__ __forceinline__ void arrive_warp(uint64_t* bar) {
   if (lane_id() == 0) mbar_arrive(bar);
 }
 
-// Weight of row r of a chunk with n real rows, `more` rows before the place it is decayed to.
+// Weight of row r of a chunk with n real rows, `more` rows before the place it is decayed to.  Rows from n on, which are
+// zeros, have a real row's weight: with decays above 1 a larger one could be infinite.
 __device__ __forceinline__ float row_weight(float l2, int r, int n, int reverse, int more) {
-  return lin_pow(l2, more + (reverse ? r + 1 : max(n - 1 - r, 0)));
+  return lin_pow(l2, more + (reverse ? min(r + 1, n) : max(n - 1 - r, 0)));
 }
 
 constexpr int kHalf = kChunk / 2;  // rows whose second and third parts are held at a time
