@@ -105,3 +105,12 @@ def test_broadcast_outputs(flat):
                          ids=["no pool", "no entries", "negative entries", "fewer entries than rows", "entries overlap"])
 def test_step(kw):
     assert step(cfg(**kw)) == INVALID
+
+
+@pytest.mark.parametrize("tokens", [-7, 1 << 30, 0, 5])
+def test_step_does_not_read_tokens(tokens):
+    """Whatever cfg.tokens holds, the step goes on to its later checks (here: an output that is an input)."""
+    same = (at(0), *GOOD)
+    assert step(cfg(state_out=STATE_OUT, n_slots=2, tokens=tokens), t3=same) == INVALID
+    assert step(cfg(state_out=STATE_OUT + 8, n_slots=2, tokens=tokens)) == ALIGNMENT
+    assert step(cfg(state_out=STATE_OUT, n_slots=2, tokens=tokens), t1=(at(1) + 8, *GOOD)) == ALIGNMENT

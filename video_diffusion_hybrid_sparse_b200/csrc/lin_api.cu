@@ -26,14 +26,16 @@ size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 vdn_status cuda_status(cudaError_t e) { return e == cudaSuccess ? VDN_OK : VDN_ERR_CUDA; }
 
-vdn_status check_linear(const vdn_linear_cfg* c) {
+// `step`: cfg->tokens is not read.
+vdn_status check_linear(const vdn_linear_cfg* c, bool step = false) {
   if (!c) return VDN_ERR_INVALID_ARG;
-  if (c->batch < 1 || c->tokens < 0 || c->heads < 1) return VDN_ERR_INVALID_ARG;
+  const int tokens = step ? 1 : c->tokens;
+  if (c->batch < 1 || tokens < 0 || c->heads < 1) return VDN_ERR_INVALID_ARG;
   if (c->debug_flags & ~(VDN_POISON_WS | VDN_INJECT_TIMEOUT)) return VDN_ERR_INVALID_ARG;
   if (c->head_dim != 32 && c->head_dim != 64 && c->head_dim != 128) return VDN_ERR_UNSUPPORTED;
   if (c->dtype != VDN_BF16 && c->dtype != VDN_FP32) return VDN_ERR_UNSUPPORTED;
   // row coordinates and counts of (batch, head) pairs are 32-bit
-  if (c->heads > 4096 || (long long)c->batch * c->heads >= (1ll << 24) || c->tokens >= (1 << 30))
+  if (c->heads > 4096 || (long long)c->batch * c->heads >= (1ll << 24) || tokens >= (1 << 30))
     return VDN_ERR_UNSUPPORTED;
   return VDN_OK;
 }
@@ -351,7 +353,7 @@ vdn_status vdn_linear_attn_bwd(const vdn_view* q, const vdn_view* k, const vdn_v
 vdn_status vdn_linear_attn_step(const vdn_view* q, const vdn_view* k, const vdn_view* v, const vdn_view* out,
                                 const vdn_linear_cfg* cfg, void* stream) {
   NvtxRange nvtx("vdn:linear_attn_step");
-  vdn_status s = check_linear(cfg);
+  vdn_status s = check_linear(cfg, true);
   if (s == VDN_OK) s = check_common(cfg);
   if (s != VDN_OK) return s;
   if (!cfg->state_out || cfg->n_slots < 1) return VDN_ERR_INVALID_ARG;
