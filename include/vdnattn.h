@@ -380,7 +380,7 @@ typedef struct {
   int32_t heads;          /* 1 <= H <= 4096 */
   int32_t head_dim;       /* d in {32, 64, 128} */
   int32_t dtype;          /* vdn_dtype of q, k, v, out and their gradients */
-  float scale;            /* <= 0 selects 1/sqrt(head_dim) */
+  float scale;            /* <= 0 selects 1/sqrt(head_dim); else a normal number */
   const float* log_decay; /* device [heads] fp32, 4-byte aligned */
   const int32_t* lengths; /* device [batch] or NULL (all tokens); not read by the step */
   const float* state_in;  /* fwd, bwd: S before the first token, or NULL (0) */

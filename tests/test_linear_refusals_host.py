@@ -114,3 +114,16 @@ def test_step_does_not_read_tokens(tokens):
     assert step(cfg(state_out=STATE_OUT, n_slots=2, tokens=tokens), t3=same) == INVALID
     assert step(cfg(state_out=STATE_OUT + 8, n_slots=2, tokens=tokens)) == ALIGNMENT
     assert step(cfg(state_out=STATE_OUT, n_slots=2, tokens=tokens), t1=(at(1) + 8, *GOOD)) == ALIGNMENT
+
+
+@pytest.mark.parametrize("scale", [float("nan"), float("inf"), 1e-40])
+def test_scales_that_are_not_numbers(scale):
+    """A scale above 0 is a normal number (its inverse enters the backward call); a NaN does not select the default."""
+    assert fwd(cfg(scale=scale)) == INVALID and bwd(cfg(scale=scale)) == INVALID
+    assert step(cfg(scale=scale, state_out=STATE_OUT, n_slots=2)) == INVALID
+    assert vb.library().vdn_linear_validate(cfg(scale=scale)) == INVALID
+
+
+@pytest.mark.parametrize("scale", [0.0, -1.0, -float("inf"), 1.2e-38, 3.4e38])
+def test_scales(scale):
+    assert vb.library().vdn_linear_validate(cfg(scale=scale)) == 0

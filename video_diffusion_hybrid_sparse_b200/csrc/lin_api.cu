@@ -31,6 +31,7 @@ vdn_status check_linear(const vdn_linear_cfg* c, bool step = false) {
   if (!c) return VDN_ERR_INVALID_ARG;
   const int tokens = step ? 1 : c->tokens;
   if (c->batch < 1 || tokens < 0 || c->heads < 1) return VDN_ERR_INVALID_ARG;
+  if (!(c->scale <= 0.f) && !std::isnormal(c->scale)) return VDN_ERR_INVALID_ARG;
   if (c->debug_flags & ~(VDN_POISON_WS | VDN_INJECT_TIMEOUT)) return VDN_ERR_INVALID_ARG;
   if (c->head_dim != 32 && c->head_dim != 64 && c->head_dim != 128) return VDN_ERR_UNSUPPORTED;
   if (c->dtype != VDN_BF16 && c->dtype != VDN_FP32) return VDN_ERR_UNSUPPORTED;
