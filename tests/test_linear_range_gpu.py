@@ -1,4 +1,4 @@
-"""The causal linear memory at the ends of its decays' range."""
+"""The causal linear memory at the ends of its decays' range, and the record of its waits that run out."""
 import pytest
 import torch
 
@@ -39,3 +39,30 @@ def test_growing_memory_of_short_sequences(N, lengths, log_decay, d, dtype):
         grads = vb.linear_attn_bwd(q, k, v, ld, do, state_in=init, d_state_out=dlast, d_state_in=din, lengths=n)
         for name, got in zip(("dq", "dk", "dv", "d_state_in"), (*grads, din)):
             R.check(got, ref[name], name, dtype, d, N)
+
+
+@pytest.mark.parametrize("backward", [False, True], ids=["fwd", "bwd"])
+@pytest.mark.parametrize("N,d", [(500, 64), (500, 128), (9000, 128)])
+def test_timeout_record(N, d, backward):
+    """The wait that the injected timeout lets run out is the one in the record: kernel 20, block 0, the warp that issues the
+    scores, 88 bytes before the flag, after 10 ms and before the limit of the other waits."""
+    q, k, v, do = tensors(1, N, 2, d, BF16, 2)
+    ld, status = torch.tensor([-0.01, -0.1], device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = torch.empty(vb.linear_workspace_bytes(1, N, 2, d, BF16, backward), dtype=torch.uint8, device="cuda")
+
+    def call(**kw):
+        if backward:
+            return vb.linear_attn_bwd(q, k, v, ld, do, workspace=ws, status=status, **kw)
+        return vb.linear_attn_fwd(q, k, v, ld, workspace=ws, status=status, **kw)
+
+    vb.clear_timeout_record(ws)
+    call(debug_flags=vb.INJECT_TIMEOUT)
+    assert int(status) == 6
+    rec = vb.timeout_record(ws)
+    assert {x: rec[x] for x in ("timeouts", "kernel", "block", "warp", "bar_off", "parity")} == {
+        "timeouts": 1, "kernel": 20, "block": 0, "warp": 1, "bar_off": 88, "parity": 0}, rec
+    assert 10_000_000 <= rec["ns"] < 1_000_000_000 and 0 <= rec["sm"] < 148
+    vb.clear_timeout_record(ws)
+    status.zero_()
+    call()
+    assert int(status) == 0 and vb.timeout_record(ws)["timeouts"] == 0

@@ -281,7 +281,8 @@ _STAGING: dict = {}
 
 _REC_FIELDS = ("timeouts", "kernel", "block", "warp", "bar_off", "parity")
 # kernel ids in the record: 1 state build, 3 softmax (bf16), 31 softmax (fp8),
-# 4 readout + merge (TMA-fed), 41 readout + merge (general)
+# 4 readout + merge (TMA-fed), 41 readout + merge (general), 20 causal linear
+# memory (bf16), 21 the states of its ranges
 
 
 def timeout_record(workspace: torch.Tensor) -> dict:
@@ -603,7 +604,9 @@ def linear_attn_fwd(q, k, v, log_decay, *, scale: float = 0.0, state_in=None, st
     of one projection serve); log_decay: [H] fp32, a constant (no gradient);
     state_in, state_out: [B, H, d, d] fp32 or None, state_out is written and may
     be state_in; lengths: [B] int32 or None, the tokens of each padded sequence:
-    rows behind them come out as zeros.  ``scale`` <= 0 selects d**-0.5."""
+    rows behind them come out as zeros.  ``scale`` <= 0 selects d**-0.5.  A kernel
+    whose wait runs out sets ``status`` (int32) to 6; its timeout record is in the
+    ``workspace`` of the call (:func:`timeout_record`) where one was given."""
     if stream is None and workspace is None:
         r = _direct().linear_fwd(q, k, v, log_decay, scale, state_in, state_out, lengths, out, status, debug_flags)
         if r is not None:
