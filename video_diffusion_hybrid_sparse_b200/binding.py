@@ -11,6 +11,7 @@ import contextlib
 import ctypes
 import functools
 import os
+import warnings
 from dataclasses import dataclass
 
 import numpy as np
@@ -468,15 +469,30 @@ _HERE = contextlib.nullcontext()
 _calls = None  # the extension module of csrc/py/calls.cpp
 
 
+class _Checked:
+    """Stands for the extension module where it cannot be used: every call is left to the code here."""
+
+    linear_fwd = linear_bwd = linear_step = norm_fwd = norm_bwd = staticmethod(lambda *args: None)
+
+
 def _direct():
     """The module that makes ordinary calls in one step (csrc/py/calls.cpp): each
-    of its functions returns None for a call that it leaves to the code here."""
+    of its functions returns None for a call that it leaves to the code here.
+    Without it, or with one of another torch, all calls are made here, on the same
+    kernels, with some microseconds more on the host."""
     global _calls
     if _calls is None:
         library()
-        from . import _calls as module
+        try:
+            from . import _calls as module
 
-        _calls = module
+            if module.torch_version != str(torch.__version__):
+                raise ImportError(f"built with torch {module.torch_version}, this is {torch.__version__}")
+            _calls = module
+        except ImportError as e:
+            warnings.warn(f"the binding's extension module is not used ({e}); rebuild with python -m "
+                          "video_diffusion_hybrid_sparse_b200.build", RuntimeWarning, stacklevel=3)
+            _calls = _Checked
     return _calls
 
 

@@ -92,20 +92,32 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     return LIB
 
 
+def _read(path: str) -> str | None:
+    try:
+        with open(path) as f:
+            return f.read()
+    except FileNotFoundError:
+        return None
+
+
 def build_calls(force: bool = False, verbose: bool = False) -> str:
-    """The extension module that makes the binding's small calls (csrc/py/calls.cpp)."""
+    """The extension module that makes the binding's small calls (csrc/py/calls.cpp).
+
+    It belongs to the torch and the Python that it was built with, whose versions
+    are kept beside the objects: times of files do not tell."""
     import torch
     from torch.utils import cpp_extension
 
     src, header = os.path.join(CSRC, "py", "calls.cpp"), os.path.join(INCLUDE, "vdnattn.h")
-    if not force and not _stale(CALLS, [src, header, torch.__file__]):
+    stamp, versions = os.path.join(BUILD, "calls.versions"), f"{torch.__version__} {sys.version}"
+    if not force and not _stale(CALLS, [src, header, torch.__file__]) and _read(stamp) == versions:
         return CALLS
     home = os.path.dirname(os.path.dirname(nvcc()))
     dirs = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"], os.path.join(home, "include"), INCLUDE]
     libs = cpp_extension.library_paths()
     cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden", "-Wno-attributes",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-I{d}" for d in dirs], src, "-o", CALLS,
-           f"-L{PKG}", "-l:libvdnattn.so", "-Wl,-rpath,$ORIGIN", *[f"-L{d}" for d in libs], "-lc10", "-lc10_cuda",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DVDN_TORCH="{torch.__version__}"',
+           *[f"-I{d}" for d in dirs], src, "-o", CALLS, f"-L{PKG}", "-l:libvdnattn.so", "-Wl,-rpath,$ORIGIN", *[f"-L{d}" for d in libs], "-lc10", "-lc10_cuda",
            "-ltorch_cpu", "-ltorch", "-ltorch_python"]
     if verbose:
         print(" ".join(cmd), flush=True)
@@ -113,6 +125,9 @@ def build_calls(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError("the binding's extension module failed to build")
+    os.makedirs(BUILD, exist_ok=True)
+    with open(stamp, "w") as f:
+        f.write(versions)
     return CALLS
 
 

@@ -333,4 +333,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nul
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__calls() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__calls() {
+  PyObject* m = PyModule_Create(&module);
+  // the torch it was built with, which the binding compares
+  if (m && PyModule_AddStringConstant(m, "torch_version", VDN_TORCH) != 0) Py_CLEAR(m);
+  return m;
+}
