@@ -416,7 +416,9 @@ VDN_API vdn_status vdn_linear_attn_bwd(const vdn_view* q, const vdn_view* k, con
  * scale * q_b S of the new state.  A negative slot marks a padding row: no state
  * is touched and its out row is written as zeros; so does a slot >= n_slots,
  * which also writes VDN_ERR_INVALID_ARG to status_word.  Rows with the same slot
- * are successive tokens of one sequence, taken in the order of the rows. */
+ * are successive tokens of one sequence, taken in the order of the rows.  To find
+ * them the slots are read batch times: for batches of thousands of rows that costs
+ * more than the states (NULL, for rows in the pool's order, does not). */
 VDN_API vdn_status vdn_linear_attn_step(const vdn_view* q, const vdn_view* k, const vdn_view* v, const vdn_view* out,
                                         const vdn_linear_cfg* cfg, void* stream);
 

@@ -684,7 +684,9 @@ def linear_attn_step(q, k, v, log_decay, state, *, slots=None, scale: float = 0.
     place; slots: [B] int32, the pool entry of each row (None: row b has entry
     b).  A negative slot marks a padding row (out is zero there, no state is
     touched), and so does one past the pool, which also sets ``status`` (int32) to
-    1.  Rows of the same slot are successive tokens, in the order of the rows."""
+    1.  Rows of the same slot are successive tokens, in the order of the rows; the
+    search for them is quadratic in B (batches of thousands: order the pool and
+    leave slots out)."""
     if stream is None:
         r = _direct().linear_step(q, k, v, log_decay, state, slots, scale, out, status)
         if r is not None:

@@ -9,7 +9,14 @@
 // over rows of column j), so small batches spread over the SMs without a join.
 // A thread owns four columns (16 bytes) of every kRows-th row and keeps them in
 // registers from the load to the store; all its loads are in flight at once.
-// Measured: 192 x 16 x 128 of a pool of 256 in 61 us, 0.91 of the copy rate.
+// Measured: 192 x 16 x 128 of a pool of 256 in 68 us as a call, 0.91 of the copy
+// rate.
+//
+// With slots, a CTA looks all of them through for rows that share its own (4 B
+// bytes, from L2, once for each of its tokens): B^2 H D / 32 reads in all, which
+// are nothing for some hundred rows and outweigh the states from about 64 D rows
+// on.  Measured, with slots and without: 700 x 1 x 32 6.1 and 6.3 us, 4096 x 16 x
+// 128 2048 and 1260, 20000 x 1 x 32 234 and 27, 65536 x 1 x 32 3860 and 87.
 #include "lin_common.cuh"
 
 namespace vdn {
