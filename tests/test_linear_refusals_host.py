@@ -3,6 +3,7 @@ of its own here, so that only the check under test can refuse the call.  No poin
 import ctypes
 
 import pytest
+import torch
 
 from video_diffusion_hybrid_sparse_b200 import binding as vb
 
@@ -127,3 +128,16 @@ def test_scales_that_are_not_numbers(scale):
 @pytest.mark.parametrize("scale", [0.0, -1.0, -float("inf"), 1.2e-38, 3.4e38])
 def test_scales(scale):
     assert vb.library().vdn_linear_validate(cfg(scale=scale)) == 0
+
+
+def test_negated_views_are_refused():
+    """A lazily negated tensor's memory holds other values than the tensor: the binding refuses it wherever it goes."""
+    t, neg = torch.ones(2, 3, 2, 32), torch._neg_view(torch.ones(2, 3, 2, 32))
+    like = (t, t.shape, t.dtype, t.get_device())
+    rows, states, vector = torch.ones(4, 8), torch.ones(2, 2, 32, 32), torch.ones(5)
+    assert vb._view("k", t, *like).data == t.data_ptr() and vb._rows("x", rows, rows, rows.dtype)[0] == rows.data_ptr()
+    for f in (lambda: vb._view("k", neg, *like), lambda: vb._rows("x", torch._neg_view(rows), rows, rows.dtype),
+              lambda: vb._state("state_in", torch._neg_view(states), 2, 2, 32, states.device),
+              lambda: vb._flat("weight", torch._neg_view(vector), 5, vector.dtype, vector.device)):
+        with pytest.raises(ValueError, match="negat"):
+            f()

@@ -513,6 +513,12 @@ def _here(t: torch.Tensor) -> int:
     return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
+def _as_stored(name, t):
+    """The memory of ``t`` holds its values (torch negates some views lazily)."""
+    if t.is_neg():
+        raise ValueError(f"{name}: a lazily negated view; call resolve_neg() on it")
+
+
 def _match(name, t, like):
     """``t`` has the shape, type and device of ``like``, and rows of contiguous elements."""
     if t.shape != like.shape or t.dtype != like.dtype or t.device != like.device:
@@ -530,6 +536,7 @@ def _new(like):
 def _view(name, t, like, shape, dtype, index) -> VdnView:
     """View of a [B, N, H, d] or (a step's) [B, H, d] tensor, checked against ``like``, whose shape, type and device
     number follow."""
+    _as_stored(name, t)
     s = t.stride()
     if t.shape != shape or t.dtype is not dtype or t.get_device() != index or s[-1] != 1:
         _match(name, t, like)
@@ -543,6 +550,7 @@ def _state(name, t, B, H, d, device):
     if t.shape != (B, H, d, d) or t.dtype != torch.float32 or t.device != device:
         raise ValueError(f"{name}: expected {(B, H, d, d)} torch.float32 on {device}, got {tuple(t.shape)} {t.dtype} "
                          f"on {t.device}")
+    _as_stored(name, t)
     s = t.stride()
     if s[1:] != (d * d, d, 1) and (H > 1 or s[2:] != (d, 1)):
         raise ValueError(f"{name}: the last three dimensions must be contiguous")
@@ -558,6 +566,7 @@ def _flat(name, t, n, dtype, device):
     if t.shape != (n,) or t.dtype != dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous ({n},) {dtype} on {device}, got {tuple(t.shape)} {t.dtype} "
                          f"on {t.device}")
+    _as_stored(name, t)
     return t.data_ptr()
 
 
@@ -714,6 +723,7 @@ def _rows(name, t, like, dtype):
     if t.shape != like.shape or t.dtype != dtype or t.device != like.device:
         raise ValueError(f"{name}: expected {tuple(like.shape)} {dtype} on {like.device}, got {tuple(t.shape)} {t.dtype} "
                          f"on {t.device}")
+    _as_stored(name, t)
     (rows, W), (s0, s1) = t.shape, t.stride()
     if s1 != 1 and W != 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
@@ -769,6 +779,7 @@ def add_rmsnorm_fwd(x, weight=None, *, residual=None, residual_out=None, eps: fl
                     or not scales.is_contiguous():
                 raise ValueError(f"scales: expected a contiguous {(rows, groups)} torch.float32 on {dev}, got "
                                  f"{tuple(scales.shape)} {scales.dtype} on {scales.device}")
+            _as_stored("scales", scales)
             ps = scales.data_ptr()
         if out is None:
             out = torch.empty_like(x, dtype=kind, memory_format=torch.contiguous_format)
