@@ -66,3 +66,28 @@ def test_timeout_record(N, d, backward):
     status.zero_()
     call()
     assert int(status) == 0 and vb.timeout_record(ws)["timeouts"] == 0
+
+
+def test_outside_autograd():
+    """No output requires a gradient; a function of the user's own carries the gradients of the two calls."""
+    B, N, H, d = 2, 70, 2, 64
+    q, k, v, do = (t.requires_grad_() for t in tensors(B, N, H, d, FP32, 3))
+    ld = torch.tensor([-0.01, -0.1], device="cuda")
+    assert not vb.linear_attn_fwd(q, k, v, ld).requires_grad
+    x = torch.randn(4, 64, device="cuda", requires_grad=True)
+    assert not vb.add_rmsnorm_fwd(x).requires_grad
+
+    class Memory(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, q, k, v, log_decay):
+            ctx.save_for_backward(q, k, v, log_decay)
+            return vb.linear_attn_fwd(q, k, v, log_decay)
+
+        @staticmethod
+        def backward(ctx, d_out):
+            return (*vb.linear_attn_bwd(*ctx.saved_tensors, d_out.contiguous()), None)
+
+    Memory.apply(q, k, v, ld).backward(do.detach())
+    ref = R.backward(q.detach(), k.detach(), v.detach(), ld, d ** -0.5, do.detach())
+    for name, t in (("dq", q), ("dk", k), ("dv", v)):
+        R.check(t.grad, ref[name], name, FP32, d, N)

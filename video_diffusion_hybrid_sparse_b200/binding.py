@@ -463,6 +463,10 @@ def validate(s: Shape, **kw) -> int:
 
 # ---------------------------------------------------------------- causal linear memory and residual RMSNorm
 
+# Like all calls here, these are outside autograd: an output carries no gradient and no forward-mode tangent, whatever its
+# inputs require, and outputs and states written in place do not count as changes of their tensors.  A training program
+# calls the forward and backward functions from a torch.autograd.Function of its own.
+
 NORM_OUT_TENSOR, NORM_OUT_E4M3_ROW, NORM_OUT_E4M3_GROUP = 0, 1, 2
 _DTYPES = {torch.bfloat16: VDN_BF16, torch.float32: VDN_FP32}
 _HERE = contextlib.nullcontext()
@@ -631,7 +635,9 @@ def linear_attn_fwd(q, k, v, log_decay, *, scale: float = 0.0, state_in=None, st
     be state_in; lengths: [B] int32 or None, the tokens of each padded sequence:
     rows behind them come out as zeros.  ``scale`` <= 0 selects d**-0.5.  A kernel
     whose wait runs out sets ``status`` (int32) to 6; its timeout record is in the
-    ``workspace`` of the call (:func:`timeout_record`) where one was given."""
+    ``workspace`` of the call (:func:`timeout_record`) where one was given.
+    Outside autograd: the output requires no gradient; :func:`linear_attn_bwd`
+    forms the gradients."""
     if stream is None and workspace is None:
         r = _direct().linear_fwd(q, k, v, log_decay, scale, state_in, state_out, lengths, out, status, debug_flags)
         if r is not None:
@@ -695,7 +701,7 @@ def linear_attn_step(q, k, v, log_decay, state, *, slots=None, scale: float = 0.
     touched), and so does one past the pool, which also sets ``status`` (int32) to
     1.  Rows of the same slot are successive tokens, in the order of the rows; the
     search for them is quadratic in B (batches of thousands: order the pool and
-    leave slots out)."""
+    leave slots out).  For serving: it has no backward form."""
     if stream is None:
         r = _direct().linear_step(q, k, v, log_decay, state, slots, scale, out, status)
         if r is not None:
@@ -759,7 +765,8 @@ def add_rmsnorm_fwd(x, weight=None, *, residual=None, residual_out=None, eps: fl
     residual, as may out in the tensors' type); weight: [W] fp32 or None (ones).  Returns y in the tensors' type,
     or, for NORM_OUT_E4M3_ROW / NORM_OUT_E4M3_GROUP, (values, scales): e4m3
     [rows, W] and fp32 scales [rows, 1] / [rows, ceil(W / 128)], y ~ value *
-    scale."""
+    scale.  Outside autograd: no output requires a gradient;
+    :func:`add_rmsnorm_bwd` forms those of the tensor output."""
     if stream is None:
         r = _direct().norm_fwd(x, weight, residual, residual_out, eps, out_mode, out, scales)
         if r is not None:
