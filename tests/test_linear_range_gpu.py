@@ -91,3 +91,33 @@ def test_outside_autograd():
     ref = R.backward(q.detach(), k.detach(), v.detach(), ld, d ** -0.5, do.detach())
     for name, t in (("dq", q), ("dk", k), ("dv", v)):
         R.check(t.grad, ref[name], name, FP32, d, N)
+
+
+def many_chunks(B, N, H, d, dtype):
+    """Decays whose memory spans some thousand chunks: the states, which are fp32, are those of the formula in norm, though
+    lambda^128 (or lambda^64) is a factor of every chunk.  A state's chain has N / 64 roundings of at most 2^-24 in no order:
+    their root mean square is below sqrt(N / 64) / sqrt(3) * 2^-24; the sums inside a chunk and (bf16) the third part's 2^-24
+    and the second's 2^-20 of a term below 2^-4 come to less than 1e-6."""
+    ld = torch.tensor([-1e-6, -3.3e-5, -1e-4, -1e-5], device="cuda")
+    g = torch.Generator("cuda").manual_seed(N)
+    # values of one sign as a state's mean: errors that all have one direction do not cancel
+    q, k, v, do = (torch.randn(B, N, H, d, device="cuda", generator=g).abs().to(dtype) for _ in range(4))
+    w = torch.exp(ld.double()[None, :] * torch.arange(N, device="cuda").double()[:, None])  # lambda^i
+    limit = (N / 64) ** 0.5 / 3 ** 0.5 * 2.0 ** -24 + 1e-6
+    state, din = (torch.empty(B, H, d, d, device="cuda") for _ in range(2))
+    vb.linear_attn_fwd(q, k, v, ld, scale=1.0, state_out=state)
+    vb.linear_attn_bwd(q, k, v, ld, do, scale=1.0, d_state_in=din)
+    for b in range(B):
+        for h in range(H):
+            s = (k[b, :, h].double() * w[:, h].flip(0)[:, None]).T @ v[b, :, h].double()
+            r = (q[b, :, h].double() * (w[:, h] * torch.exp(ld[h].double()))[:, None]).T @ do[b, :, h].double()
+            for name, got, want in (("state", state[b, h], s), ("d_state_in", din[b, h], r)):
+                e = float((got.double() - want).norm() / want.norm())
+                assert e <= limit, (name, b, h, e, limit)
+
+
+@pytest.mark.parametrize("dtype,B,N,H,d", [(FP32, 1, 100_000, 4, 64), (FP32, 2, 60_000, 4, 128), (FP32, 40, 20_000, 4, 32),
+                                           (BF16, 36, 10_000, 4, 128)])
+def test_memory_over_many_chunks(dtype, B, N, H, d):
+    """Heads in ranges and (bf16) whole ones."""
+    many_chunks(B, N, H, d, dtype)

@@ -17,6 +17,37 @@ __device__ __forceinline__ float lin_log2_decay(float log_decay) {
 // of the power: at most 1e-5 before the power itself is below 2^-126.
 __device__ __forceinline__ float lin_pow(float log2_decay, int n) { return exp2f(log2_decay * (float)n); }
 
+// lambda^n as a state is multiplied by it: s * lambda^n = base s + m s.  Where a state keeps its tokens over many such
+// products (|n log lambda| < 1/2), m is lambda^n - 1 and base 1: a rounded power, which is off by up to 2^-24 in the same
+// direction each time, is 1e-5 off after a thousand chunks, and 1e-3 after 100000 single tokens.
+struct LinFall {
+  float m, base;
+  __device__ __forceinline__ LinFall(float log_decay, int n) {
+    const float y = log_decay * (float)n;
+    const bool slow = fabsf(y) < 0.5f;
+    base = slow ? 1.f : 0.f;
+    m = slow ? expm1f(y) : lin_pow(lin_log2_decay(log_decay), n);
+  }
+  // `s` decayed, plus `a`
+  __device__ __forceinline__ float operator()(float s, float a) const { return fmaf(m, s, a) + (base != 0.f ? s : 0.f); }
+};
+
+// The same power as one factor for each of many chunks, rounded so that what one rounding leaves out the next makes up for:
+// the product of any number of them in a row is off by a rounding or two.
+class LinFactors {
+ public:
+  __device__ __forceinline__ LinFactors(float log_decay, int n) : f_(log_decay, n), left_(0.f) {}
+  __device__ __forceinline__ float next() {
+    const float t = f_.m + left_, g = f_.base + t;
+    left_ = t - (g - f_.base);
+    return g;
+  }
+
+ private:
+  LinFall f_;
+  float left_;
+};
+
 __device__ __forceinline__ int lin_length(const int* lengths, int b, int N) {
   return lengths ? min(max(lengths[b], 0), N) : N;
 }

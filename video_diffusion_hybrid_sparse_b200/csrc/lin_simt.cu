@@ -199,9 +199,10 @@ __global__ void __launch_bounds__(kThreads) lin_states_simt(const __grid_constan
   const long long t0 = cuts.start(range), t1 = cuts.start(range + 1);
   const int bh = (int)((t1 - 1) / pl.nc), b = bh / p.H, h = bh % p.H, len = lin_length(p.lengths, b, p.N);
   const long long head0 = (long long)bh * pl.nc;
-  const float l2 = lin_log2_decay(p.log_decay[h]);
+  const float log_decay = p.log_decay[h], l2 = lin_log2_decay(log_decay);
   const LinStretch st = lin_piece_of(lin_stretch((int)(max(t0, head0) - head0), (int)(t1 - head0), len, l2, pl, wk.reverse), blockIdx.x % pl.sub, pl);
   if (st.u0 == st.u1) return;
+  LinFactors whole(log_decay, kC);
   StateTile<D> W;
   W.zero();
   for (int u = st.u0; u < st.u1; ++u) {
@@ -210,7 +211,7 @@ __global__ void __launch_bounds__(kThreads) lin_states_simt(const __grid_constan
     load_rows<T, D>(Y, wk.y, b, h, row0, n);
     load_rows<T, D>(Z, wk.z, b, h, row0, n);
     row_weights(w, l2, n, wk.reverse);
-    const float fall = lin_pow(l2, n);
+    const float fall = n == kC ? whole.next() : lin_pow(l2, n);
 #pragma unroll
     for (int i = 0; i < W.kT; ++i)
 #pragma unroll
@@ -246,7 +247,8 @@ __global__ void __launch_bounds__(kThreads) lin_out_simt(const __grid_constant__
     const LinPiece pc(t, t_end, pl);
     t += pc.u1 - pc.u0;
     const int b = pc.bh / p.H, h = pc.bh % p.H, len = lin_length(p.lengths, b, p.N);
-    const float l2 = lin_log2_decay(p.log_decay[h]);
+    const float log_decay = p.log_decay[h], l2 = lin_log2_decay(log_decay);
+    LinFactors whole(log_decay, kC);
     __syncthreads();
     if (tid <= kC) pw[tid] = lin_pow(l2, tid);
     const float* src = nullptr;
@@ -312,7 +314,7 @@ __global__ void __launch_bounds__(kThreads) lin_out_simt(const __grid_constant__
         StateTile<D> S;
         S.zero();
         S.add(Y, Z, w, n);
-        const float fall = pw[n];
+        const float fall = n == kC ? whole.next() : pw[n];
 #pragma unroll
         for (int i = 0; i < S.kT; ++i)
 #pragma unroll
@@ -355,9 +357,9 @@ __global__ void __launch_bounds__(128) lin_scan(const __grid_constant__ LinState
   const int j0 = head.first, j1 = head.last;
   if (j1 == j0) return;
   const int len = lin_length(p.lengths, b, p.N);
-  const float l2 = lin_log2_decay(p.log_decay[h]);
+  const float log_decay = p.log_decay[h], l2 = lin_log2_decay(log_decay);
   // the head's ranges j0 .. j1 - 1: decay over each, and whether the pieces of its part have been written
-  __shared__ float fall[kLinMaxGrid];
+  __shared__ float2 fall[kLinMaxGrid];
   __shared__ bool has[kLinMaxGrid * kLinMaxSub];
   const int n = (j1 - j0) * sub;
   for (int i = threadIdx.x; i < n; i += blockDim.x) {
@@ -365,8 +367,10 @@ __global__ void __launch_bounds__(128) lin_scan(const __grid_constant__ LinState
     const int u0 = cuts.start_in(head, bh, j), u1 = cuts.start_in(head, bh, j + 1);
     const LinStretch st = lin_piece_of(lin_stretch(u0, u1, len, l2, pl, wk.reverse), i & (sub - 1), pl);
     has[i] = st.u0 < st.u1;
-    if ((i & (sub - 1)) == 0)
-      fall[i >> lg] = lin_pow(l2, lin_rows(u0, u1, len, pl, wk.reverse));
+    if ((i & (sub - 1)) == 0) {
+      const LinFall f(log_decay, lin_rows(u0, u1, len, pl, wk.reverse));
+      fall[i >> lg] = make_float2(f.m, f.base);
+    }
   }
   __syncthreads();
   pdl_wait();
@@ -402,9 +406,9 @@ __global__ void __launch_bounds__(128) lin_scan(const __grid_constant__ LinState
     for (int i = 0; i < kAhead; ++i) {
       if (i0 + i >= n) continue;
       const int k = (i0 + i) >> lg, part = (i0 + i) & (sub - 1);
-      const float f = part == 0 ? fall[k] : 1.f;
+      const float2 f = part == 0 ? fall[k] : make_float2(1.f, 0.f);
 #pragma unroll
-      for (int x = 0; x < kE; ++x) s[x] = fmaf(f, s[x], a[i][x]);
+      for (int x = 0; x < kE; ++x) s[x] = fmaf(f.x, s[x], a[i][x]) + (f.y != 0.f ? s[x] : 0.f);
       if (part == sub - 1) store(wk.s_in + (long long)(j0 + k + 1) * DD + e, s);
     }
   }

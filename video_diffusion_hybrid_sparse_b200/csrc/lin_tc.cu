@@ -625,7 +625,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lin_out_tc(const __grid_constan
       const int b = pc.bh / p.H, h = pc.bh % p.H, len = lin_length(p.lengths, b, p.N);
       int ua, ub;
       lin_real(pc.u0, pc.u1, len, pl, rev, ua, ub);
-      const float l2 = lin_log2_decay(p.log_decay[h]);
+      const float log_decay = p.log_decay[h], l2 = lin_log2_decay(log_decay);
       __nv_bfloat16* o = out_base + b * jb.o.sb + h * jb.o.sh;
       // chunks behind the sequence
 #pragma unroll 1
@@ -668,7 +668,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) lin_out_tc(const __grid_constan
           }
         }
       }
-      const float f_whole = alpha * lin_pow(l2, rev ? kChunk - 1 - r : r + 1), g_whole = lin_pow(l2, kChunk);
+      const float f_whole = alpha * lin_pow(l2, rev ? kChunk - 1 - r : r + 1);
+      LinFactors g_whole(log_decay, kChunk);
       if (ua < ub) publish();
       for (int u = ua; u < ub; ++u, ++c) {
         const int row0 = (rev ? pl.nc - 1 - u : u) * kChunk, n = min(len - row0, kChunk);
@@ -713,7 +714,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lin_out_tc(const __grid_constan
           tma_store_4d(om.map, stage, z0, h * (int)om.mh, row0 + q * 32, b * (int)om.mb);
         if (__any_sync(0xffffffffu, !lin_wait(&bars[kDwFull], ph, ab))) { ok = false; break; }
         tc_fence_after();
-        const float g = n == kChunk ? g_whole : lin_pow(l2, n);
+        const float g = n == kChunk ? g_whole.next() : lin_pow(l2, n);
         const uint64_t g2 = f32x2_pack(g, g);
         if (q * 32 < D) {
 #pragma unroll
