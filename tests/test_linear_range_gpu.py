@@ -121,3 +121,23 @@ def many_chunks(B, N, H, d, dtype):
 def test_memory_over_many_chunks(dtype, B, N, H, d):
     """Heads in ranges and (bf16) whole ones."""
     many_chunks(B, N, H, d, dtype)
+
+
+def test_memory_over_many_single_tokens():
+    """20000 single tokens: the state is that of the formula in norm, though it is multiplied by lambda once a token.  Each
+    of a state's n products is rounded by at most 2^-24 of it, in no order (new keys move it by many roundings): their root
+    mean square is below sqrt(n / 3) 2^-24 of the last state's, whose predecessors are not larger.  expm1 is good to 2^-23
+    of log_decay, which is 2^-23 n |log_decay| of the oldest term."""
+    n, d = 20000, 64
+    ld = torch.tensor([-1e-6, -3e-6, -3.3e-5, -2e-4], device="cuda")
+    g = torch.Generator("cuda").manual_seed(1)
+    q, k, v = (torch.randn(n, 1, 4, d, device="cuda", generator=g) for _ in range(3))
+    pool, out = torch.zeros(1, 4, d, d, device="cuda"), torch.empty(1, 4, d, device="cuda")
+    for i in range(n):
+        vb.linear_attn_step(q[i], k[i], v[i], ld, pool, out=out)
+    for h in range(4):
+        w = torch.exp(ld[h].double() * torch.arange(n - 1, -1, -1, device="cuda").double())
+        want = (k[:, 0, h].double() * w[:, None]).T @ v[:, 0, h].double()
+        e = float((pool[0, h].double() - want).norm() / want.norm())
+        limit = (n / 3) ** 0.5 * 2.0 ** -24 + 2.0 ** -23 * n * abs(float(ld[h]))
+        assert e <= limit, (h, e, limit)

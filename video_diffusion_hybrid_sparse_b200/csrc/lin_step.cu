@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(kStepThreads) lin_step(const __grid_constant__
   float4 s[kN];
 #pragma unroll
   for (int i = 0; i < kN; ++i) s[i] = *reinterpret_cast<const float4*>(S + (r0 + kRows * i) * D + c0);
-  const float lambda = lin_pow(lin_log2_decay(p.log_decay[h]), 1);
+  const LinFall decayed(p.log_decay[h], 1);
   int b = b0;
   while (true) {
     if (tid == 0) s_next = p.B;
@@ -90,10 +90,10 @@ __global__ void __launch_bounds__(kStepThreads) lin_step(const __grid_constant__
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
       const float k = sk[r0 + kRows * i], q = sq[r0 + kRows * i];
-      s[i].x = fmaf(lambda, s[i].x, k * v[0]);
-      s[i].y = fmaf(lambda, s[i].y, k * v[1]);
-      s[i].z = fmaf(lambda, s[i].z, k * v[2]);
-      s[i].w = fmaf(lambda, s[i].w, k * v[3]);
+      s[i].x = decayed(s[i].x, k * v[0]);
+      s[i].y = decayed(s[i].y, k * v[1]);
+      s[i].z = decayed(s[i].z, k * v[2]);
+      s[i].w = decayed(s[i].w, k * v[3]);
       o[0] = fmaf(q, s[i].x, o[0]);
       o[1] = fmaf(q, s[i].y, o[1]);
       o[2] = fmaf(q, s[i].z, o[2]);
