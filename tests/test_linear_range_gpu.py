@@ -141,3 +141,22 @@ def test_memory_over_many_single_tokens():
         e = float((pool[0, h].double() - want).norm() / want.norm())
         limit = (n / 3) ** 0.5 * 2.0 ** -24 + 2.0 ** -23 * n * abs(float(ld[h]))
         assert e <= limit, (h, e, limit)
+
+
+@pytest.mark.parametrize("B,N,d", [(1, 100_000, 64), (2, 60_000, 128), (40, 20_000, 32), (8, 60_000, 64), (1, 241_920, 128)])
+def test_sums_over_many_chunks(B, N, d):
+    """bf16 heads in ranges, whose states are summed over dozens of chunks on the tensor cores."""
+    many_chunks(B, N, 4, d, BF16)
+
+
+def test_sums_without_decay():
+    """The same without a decay, where the keys' first part is all of them."""
+    B, N, H, d = 8, 60_000, 4, 64
+    ld, g = torch.zeros(H, device="cuda"), torch.Generator("cuda").manual_seed(N)
+    q, k, v, do = (torch.randn(B, N, H, d, device="cuda", generator=g).abs().to(BF16) for _ in range(4))
+    state, din = (torch.empty(B, H, d, d, device="cuda") for _ in range(2))
+    vb.linear_attn_fwd(q, k, v, ld, scale=1.0, state_out=state)
+    vb.linear_attn_bwd(q, k, v, ld, do, scale=1.0, d_state_in=din)
+    for got, y, z in ((state, k, v), (din, q, do)):
+        want = torch.einsum("nhi,nhj->hij", y[0].double(), z[0].double())
+        assert float((got[0].double() - want).norm() / want.norm()) <= (N / 64) ** 0.5 / 3 ** 0.5 * 2.0 ** -24 + 1e-6

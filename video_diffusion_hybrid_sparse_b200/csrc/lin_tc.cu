@@ -262,23 +262,28 @@ __device__ __forceinline__ void mma_columns(uint32_t acc, uint32_t a, uint32_t b
   }
 }
 
-// dW (+)= (Y1 + Y2 + ..)^T Z over 64 rows of a chunk, of n_parts parts: y, z at their first row, parts as decay_half leaves
-// them (D = 64: rows 64-127 of the transposed operand are the zero block, which stays where it is from one 16-row step to
-// the next)
+// dW (+)= Yk^T Z over 64 rows of a chunk, Yk one part of Y from its first row on, boxes of 64 columns `a_stride` apart, z at
+// its first row (D = 64: rows 64-127 of the transposed operand are the zero block, which stays where it is from one 16-row
+// step to the next)
 template <int D>
-__device__ __forceinline__ void mma_state(uint32_t acc, uint32_t y, uint32_t parts, uint32_t zero, uint32_t z, uint32_t go,
-                                          int n_parts) {
+__device__ __forceinline__ void mma_part(uint32_t acc, uint32_t a, uint32_t a_stride, uint32_t zero, uint32_t z, uint32_t go) {
   constexpr uint32_t idesc = idesc_bf16_f32(128, D, 1, 1);
   constexpr uint64_t step = D == 64 ? 128ull - (128ull << 16) : 128ull;
   const uint64_t dz = smem_desc(z, kChunk * 128, 1024, kLayoutSw128);
+  const uint64_t da = smem_desc(a, D == 64 ? zero - a : a_stride, 1024, kLayoutSw128);
 #pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    if (k == 2 && n_parts < 3) break;
-    const uint32_t a = k == 0 ? y : parts + (k - 1) * (kHalf * D * 2);
-    const uint64_t da = smem_desc(a, D == 64 ? zero - a : k == 0 ? kChunk * 128 : kHalf * 128, 1024, kLayoutSw128);
-#pragma unroll
-    for (int kk = 0; kk < kHalf / 16; ++kk) mma_ss(acc, da + kk * step, dz + kk * 128, idesc, k || kk || go);
-  }
+  for (int kk = 0; kk < kHalf / 16; ++kk) mma_ss(acc, da + kk * step, dz + kk * 128, idesc, kk || go);
+}
+// The parts behind the first, as decay_half leaves them, and the first.  An accumulator cuts what it adds at its own last
+// bit, and in one direction: the small parts come before the first one, and an accumulator has one chunk.
+template <int D>
+__device__ __forceinline__ void mma_small(uint32_t acc, uint32_t parts, uint32_t zero, uint32_t z, uint32_t go, int n_parts) {
+  if (n_parts == 3) mma_part<D>(acc, parts + kHalf * D * 2, kHalf * 128, zero, z, go);
+  mma_part<D>(acc, parts, kHalf * 128, zero, z, n_parts == 3 || go);
+}
+template <int D>
+__device__ __forceinline__ void mma_first(uint32_t acc, uint32_t y, uint32_t zero, uint32_t z) {
+  mma_part<D>(acc, y, kChunk * 128, zero, z, 1);
 }
 
 // Stores a box of shared memory through a tensor map; this thread's stores have read their memory after store_wait.
@@ -460,17 +465,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) lin_out_tc(const __grid_constan
           const int n_parts = parts_of[ph];  // as the decay warps have decided
           if (n_parts == 3) {
             if (elect_one()) {
-              mma_state<D>(tmem + kColDw, ty, base + L::kLo, base + L::kZero, tz, 0, 3);
+              mma_small<D>(tmem + kColDw, base + L::kLo, base + L::kZero, tz, 0, 3);
+              mma_first<D>(tmem + kColDw, ty, base + L::kZero, tz);
               mma_commit(&bars[kYFree]);
             }
             __syncwarp();
           }
           if (!wait(&bars[kYReady2], ph)) break;
           if (elect_one()) {
-            if (n_parts == 2) mma_state<D>(tmem + kColDw, ty, base + L::kLo, base + L::kZero, tz, 0, 2);
-            mma_state<D>(tmem + kColDw, ty + kHalf * 128, base + L::kLo + (n_parts == 2 ? kHalf * D * 2 : 0),
-                         base + L::kZero, tz + kHalf * 128, 1, n_parts);
-            if (n_parts == 2) mma_commit(&bars[kYFree]);
+            if (n_parts == 2) mma_small<D>(tmem + kColDw, base + L::kLo, base + L::kZero, tz, 0, 2);
+            mma_small<D>(tmem + kColDw, base + L::kLo + (n_parts == 2 ? kHalf * D * 2 : 0), base + L::kZero,
+                         tz + kHalf * 128, 1, n_parts);
+            if (n_parts == 2) {
+              mma_first<D>(tmem + kColDw, ty, base + L::kZero, tz);
+              mma_commit(&bars[kYFree]);
+            }
+            mma_first<D>(tmem + kColDw, ty + kHalf * 128, base + L::kZero, tz + kHalf * 128);
             mma_commit(&bars[kEmpty + y.slot]);
             mma_commit(&bars[kEmpty + z.slot]);
             mma_commit(&bars[kDwFull]);
@@ -782,8 +792,9 @@ struct StLayout {
 static_assert(StLayout<128>::kBytes <= 232448 && StLayout<64>::kBytes <= 232448, "shared memory of an SM");
 enum { sFull = 0, sEmpty = 8, sReady = 16, sLoFree = 18, sAccFull = 20, sAccFree = 22, sDone = 24, sNumBars };
 static_assert(sNumBars * 8 + 8 + sizeof(WaitRecord) <= 272, "barrier block");
-constexpr int kStWorkers = 512;  // decay warps 2-17
-constexpr int kStThreads = 64 + kStWorkers + 128;
+constexpr int kStThreads = kTcThreads;  // roles as above: decay warps 4-19, warps 20-27 add up
+constexpr uint32_t kStDecayRegs = 56, kStOutRegs = 112;
+static_assert(128 * kCtlRegs + kDecay * kStDecayRegs + kOut * kStOutRegs <= kStThreads * kTcRegs, "registers of a CTA");
 
 // One of the pieces that a CTA of the ranges' states goes through.
 struct StPiece {
@@ -815,8 +826,9 @@ static_assert(sizeof(StPiece) == 48, "room in shared memory");
 // part = sum over a range's stretch (linear.h) of the rows' w y^T z, w the decay to the stretch's end, in pieces.  A chunk
 // whose decay to there is below fp32's range adds nothing and is not read: a head that forgets within some hundred tokens
 // costs a few chunks, whatever the range.  A CTA goes through pieces gridDim apart, so that heads share the SMs evenly;
-// loads run ahead into the next piece, and two accumulators let its products start while warps 18-21 read the last one
-// out.  Two tiles a chunk (64 KB at head_dim 128).
+// loads run ahead into the next piece.  A chunk's products have one of two accumulators in turn, which warps 20-27 read out
+// and add up in registers, where sums round to nearest: one accumulator over a whole piece cuts its sum at every step and
+// was up to 4e-5 off after 80 chunks (without a decay 3e-5).  Two tiles a chunk (64 KB at head_dim 128).
 template <int D>
 __global__ void __launch_bounds__(kStThreads, 1) lin_states_tc(const __grid_constant__ LinTcMaps maps,
                                                                const __grid_constant__ LinStateParams p) {
@@ -839,10 +851,10 @@ __global__ void __launch_bounds__(kStThreads, 1) lin_states_tc(const __grid_cons
       mbar_init(&bars[sEmpty + s], 1);
     }
     for (int a = 0; a < 2; ++a) {
-      mbar_init(&bars[sReady + a], kStWorkers / 32);
+      mbar_init(&bars[sReady + a], kDecay / 32);
       mbar_init(&bars[sLoFree + a], 1);
       mbar_init(&bars[sAccFull + a], 1);
-      mbar_init(&bars[sAccFree + a], 4);
+      mbar_init(&bars[sAccFree + a], kOut / 32);
     }
     mbar_init(&bars[sDone], 1);
     ab->given_up = 0;
@@ -866,8 +878,9 @@ __global__ void __launch_bounds__(kStThreads, 1) lin_states_tc(const __grid_cons
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 0) {
-    if (lane == 0) {
+  if (warp < 4) {
+    regs_dec<kCtlRegs>();
+    if (warp == 0 && lane == 0) {
       int i = 0;
       bool ok = true;
       for (int k = 0; k < n_pieces && ok; ++k) {
@@ -890,46 +903,46 @@ __global__ void __launch_bounds__(kStThreads, 1) lin_states_tc(const __grid_cons
       if (!ok)
         for (int k = (i > L::kSlots ? i - L::kSlots : 0); k < i; ++k)
           mbar_drain(&bars[sFull + k % L::kSlots], (k / L::kSlots) & 1);
-    }
-  } else if (warp == 1) {
-    const uint32_t base = smem_u32(smem);
-    auto wait = [&](uint64_t* bar, uint32_t ph) {
-      const bool got = __all_sync(0xffffffffu, lin_wait(bar, ph, ab));
-      tc_fence_after();
-      return got;
-    };
-    bool ok = true;
-    int c = 0, done = 0;  // chunks; pieces
-    for (int k = 0; k < n_pieces && ok; ++k) {
-      const StPiece& pc = pieces[k];
-      if (pc.u0 == pc.u1) continue;
-      const int buf = done & 1;
-      if (done > 1 && !(ok = wait(&bars[sAccFree + buf], ((done >> 1) & 1) ^ 1))) break;
-      const uint32_t acc = tmem + buf * 128;
-      for (int u = pc.u0; u < pc.u1 && ok; ++u, ++c) {
-        const int ty = 2 * c, tz = ty + 1;
-        const int n_parts = third_part(pc.l2, lin_rows(u + 1, pc.end, pc.len, pl, pc.rev)) ? 3 : 2;
-        if (!(ok = wait(&bars[sFull + tz % L::kSlots], (tz / L::kSlots) & 1))) break;
-        if (!(ok = wait(&bars[sReady + (c & 1)], (c >> 1) & 1))) break;
-        const uint32_t y = base + ty % L::kSlots * L::kTile, z = base + tz % L::kSlots * L::kTile;
-        if (elect_one()) {
+    } else if (warp == 1) {
+      const uint32_t base = smem_u32(smem);
+      auto wait = [&](uint64_t* bar, uint32_t ph) {
+        const bool got = __all_sync(0xffffffffu, lin_wait(bar, ph, ab));
+        tc_fence_after();
+        return got;
+      };
+      bool ok = true;
+      int c = 0;  // chunks
+      for (int k = 0; k < n_pieces && ok; ++k) {
+        const StPiece& pc = pieces[k];
+        for (int u = pc.u0; u < pc.u1 && ok; ++u, ++c) {
+          const int ty = 2 * c, tz = ty + 1, buf = c & 1;
+          const uint32_t acc = tmem + buf * 128;
+          const int n_parts = third_part(pc.l2, lin_rows(u + 1, pc.end, pc.len, pl, pc.rev)) ? 3 : 2;
+          if (c > 1 && !(ok = wait(&bars[sAccFree + buf], ((c >> 1) & 1) ^ 1))) break;
+          if (!(ok = wait(&bars[sFull + tz % L::kSlots], (tz / L::kSlots) & 1))) break;
+          if (!(ok = wait(&bars[sReady + buf], (c >> 1) & 1))) break;
+          const uint32_t y = base + ty % L::kSlots * L::kTile, z = base + tz % L::kSlots * L::kTile;
+          if (elect_one()) {
 #pragma unroll 1
-          for (int a = 0; a < 2; ++a)
-            mma_state<D>(acc, y + a * kHalf * 128, base + L::parts(c, a, n_parts == 3), base + L::kZero,
-                         z + a * kHalf * 128, u > pc.u0 || a > 0, n_parts);
-          mma_commit(&bars[sEmpty + ty % L::kSlots]);
-          mma_commit(&bars[sEmpty + tz % L::kSlots]);
-          mma_commit(&bars[sLoFree + (c & 1)]);
-          if (u + 1 == pc.u1) mma_commit(&bars[sAccFull + buf]);
+            for (int a = 0; a < 2; ++a)
+              mma_small<D>(acc, base + L::parts(c, a, n_parts == 3), base + L::kZero, z + a * kHalf * 128, a, n_parts);
+#pragma unroll 1
+            for (int a = 0; a < 2; ++a)
+              mma_first<D>(acc, y + a * kHalf * 128, base + L::kZero, z + a * kHalf * 128);
+            mma_commit(&bars[sEmpty + ty % L::kSlots]);
+            mma_commit(&bars[sEmpty + tz % L::kSlots]);
+            mma_commit(&bars[sLoFree + buf]);
+            mma_commit(&bars[sAccFull + buf]);
+          }
+          __syncwarp();
         }
-        __syncwarp();
       }
-      ++done;
+      if (elect_one()) mma_commit(&bars[sDone]);
+      __syncwarp();
     }
-    if (elect_one()) mma_commit(&bars[sDone]);
-    __syncwarp();
-  } else if (warp < 2 + kStWorkers / 32) {
-    const int tid = threadIdx.x - 64;
+  } else if (warp < 4 + kDecay / 32) {
+    regs_dec<kStDecayRegs>();
+    const int tid = threadIdx.x - 128;
     bool ok = true;
     int c = 0;
     bool both = false;  // the chunk before takes both tiles of parts
@@ -949,7 +962,7 @@ __global__ void __launch_bounds__(kStThreads, 1) lin_states_tc(const __grid_cons
           break;
         }
         both = third;
-        if (n < kChunk) clear_rows<D, kStWorkers>(smem + tz % L::kSlots * L::kTile, tid, n);
+        if (n < kChunk) clear_rows<D, kDecay>(smem + tz % L::kSlots * L::kTile, tid, n);
 #pragma unroll 1
         for (int a = 0; a < 2; ++a)
           decay_half<D>(smem + ty % L::kSlots * L::kTile, smem + L::parts(c, a, third), a * kHalf, tid,
@@ -959,31 +972,48 @@ __global__ void __launch_bounds__(kStThreads, 1) lin_states_tc(const __grid_cons
       }
     }
   } else {
-    // read-out of finished pieces: a thread has a row
-    const int q = warp & 3, r = q * 32 + lane, d = D == 128 ? 128 : p.d;
-    int done = 0;
-    for (int k = 0; k < n_pieces; ++k) {
+    // sums of the chunks' products: a thread has half a row
+    regs_inc<kStOutRegs>();
+    const int q = warp & 3, half = (warp - 4 - kDecay / 32) >> 2;
+    constexpr int kCols = D / 2;
+    const int r = q * 32 + lane, z0 = half * kCols, d = D == 128 ? 128 : p.d;
+    uint64_t W[kCols / 2];  // pairs of columns
+    bool ok = true;
+    int c = 0;
+    for (int k = 0; k < n_pieces && ok; ++k) {
       const StPiece& pc = pieces[k];
       if (pc.u0 == pc.u1) continue;
-      const int buf = done & 1;
-      if (__any_sync(0xffffffffu, !lin_wait(&bars[sAccFull + buf], (done >> 1) & 1, ab))) break;
-      tc_fence_after();
-      float* dst = pc.wk->parts + (long long)pc.slot * d * d + (long long)r * d;
-#pragma unroll 1
-      for (int e = 0; e < D; e += 16) {
-        uint32_t x[16];
-        tmem_ld16(tmem_addr(tmem + buf * 128, q * 32, e), x);
-        tmem_wait_ld();
-        if (r < d && e < d) {
 #pragma unroll
-          for (int i = 0; i < 16; i += 4)
-            *reinterpret_cast<float4*>(dst + e + i) = make_float4(__uint_as_float(x[i]), __uint_as_float(x[i + 1]),
-                                                                  __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
+      for (int e = 0; e < kCols / 2; ++e) W[e] = 0;
+      for (int u = pc.u0; u < pc.u1; ++u, ++c) {
+        const int buf = c & 1;
+        if (__any_sync(0xffffffffu, !lin_wait(&bars[sAccFull + buf], (c >> 1) & 1, ab))) { ok = false; break; }
+        tc_fence_after();
+        if (q * 32 < D) {
+#pragma unroll
+          for (int e = 0; e < kCols; e += 16) {
+            uint32_t x[16];
+            tmem_ld16(tmem_addr(tmem + buf * 128, q * 32, z0 + e), x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; i += 2)
+              W[(e + i) / 2] = f32x2_add(W[(e + i) / 2], f32x2_pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])));
+          }
+        }
+        tc_fence_before();
+        arrive_warp(&bars[sAccFree + buf]);
+      }
+      if (ok && r < d && z0 < d) {
+        float* dst = pc.wk->parts + (long long)pc.slot * d * d + (long long)r * d + z0;
+#pragma unroll
+        for (int e = 0; e < kCols; e += 4) {
+          float v[4];
+          f32x2_unpack(W[e / 2], v[0], v[1]);
+          f32x2_unpack(W[e / 2 + 1], v[2], v[3]);
+          *reinterpret_cast<float4*>(dst + e) = make_float4(v[0], v[1], v[2], v[3]);
         }
       }
-      tc_fence_before();
-      arrive_warp(&bars[sAccFree + buf]);
-      ++done;
+      __syncwarp();
     }
   }
   tc_fence_before();
@@ -1012,7 +1042,7 @@ cudaError_t out_tc(const LinTcMaps& m, const LinOutParams& p, cudaStream_t st) {
 template <int D>
 cudaError_t states_tc(const LinTcMaps& m, const LinStateParams& p, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
-  const cudaError_t e = lin_prepare((const void*)lin_states_tc<D>, StLayout<D>::kBytes, 0, done);
+  const cudaError_t e = lin_prepare((const void*)lin_states_tc<D>, StLayout<D>::kBytes, kTcRegs, done);
   if (e != cudaSuccess) return e;
   const int pieces = p.n_walks * p.pl.grid * p.pl.sub;
   if (pieces > kStMost * kLinSms) return cudaErrorInvalidValue;  // no plan has more
