@@ -14,12 +14,15 @@
 // state is kept in two or three bf16 parts (16 or 24 bits), because a state is
 // read by every later token.
 //
-// A chunk reads three tiles and writes one (128 KB at head_dim 128: 2.9 us of a
-// 148th of the HBM rate, 5200 cycles) against 2560 cycles of products; TMA keeps
-// the next chunk's tiles in flight in a ring of slots.  Measured: 7000 cycles at
-// 128 columns, 4700 at 64 (241920 x 4 x 128: 213 us; the scan and the parts of
-// the ranges beside).  Bound by shared memory, 85 % of its cycles at 128
-// columns, and by the issue of the warps' instructions, 0.60-0.63 a cycle.
+// A chunk reads three tiles and writes one (128 KB at head_dim 128: 3.0 us of a
+// 148th of the HBM rate, 5500 cycles at 1.85 GHz) against 2560 cycles of
+// products; TMA keeps the next chunk's tiles in flight in a ring of slots.
+// Measured: 7000 cycles at 128 columns, 4700 at 64 (241920 x 4 x 128: 210 us; the
+// scan and the parts of the ranges, 91 us, beside).  Bound by shared memory, 85 %
+// of its cycles at 128 columns, and by the issue of the warps' instructions,
+// 0.54-0.56 a cycle.  A memory that spans the whole sequence (log_decay -1e-5)
+// takes 262 us and 165: no chunk falls out of the parts, and every chunk of the
+// CTAs that end a head has a third part.
 //
 // Roles (28 warps): warp 0 TMA, warps 1-2 issue the products, warps 4-19 decay
 // (P in TMEM, then Y: its first part in place, the others beside), warps 20-27
@@ -35,7 +38,7 @@
 // 64 cycles), so that every other access lengthens the chunk: arrivals are one
 // a warp, output rows leave by TMA, and the decayed Y has a third part only
 // where the state is handed out (two: states 2.4e-6 off, which the bf16 read
-// of W does not see; three: 3e-7, as fp32 sums are).
+// of W does not see; three: 4e-7 and less, as fp32 sums are).
 //
 // The roles' loops run at once and share an instruction cache of about 32 KB:
 // loops over halves and rows stay rolled and waits are short.  The products are
