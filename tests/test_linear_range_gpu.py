@@ -160,3 +160,33 @@ def test_sums_without_decay():
     for got, y, z in ((state, k, v), (din, q, do)):
         want = torch.einsum("nhi,nhj->hij", y[0].double(), z[0].double())
         assert float((got[0].double() - want).norm() / want.norm()) <= (N / 64) ** 0.5 / 3 ** 0.5 * 2.0 ** -24 + 1e-6
+
+
+@pytest.mark.parametrize("log_decay", [0.0, -1e-6, -0.004, -0.3, -0.7, 0.001])
+def test_infinite_state_elements_stay(log_decay):
+    """lambda S of an infinite element is that element, at a token, at a chunk and over a range; its neighbours are finite."""
+    ld = torch.full((2,), log_decay, device="cuda")
+    g = torch.Generator("cuda").manual_seed(2)
+
+    def with_infinities(B, d):
+        s = torch.randn(B, 2, d, d, device="cuda", generator=g)
+        s[0, 0, 3, 5], s[-1, 1, 0, d - 1] = float("inf"), -float("inf")
+        return s
+
+    for d in (32, 64, 128):
+        pool = with_infinities(3, d)
+        keep = pool.clone()
+        q, k, v = (torch.randn(3, 2, d, device="cuda", generator=g) for _ in range(3))
+        vb.linear_attn_step(q, k, v, ld, pool)
+        assert torch.equal(pool.isinf(), keep.isinf()) and torch.equal(pool[pool.isinf()], keep[keep.isinf()])
+        assert not pool.isnan().any()
+    for dtype, B, N, d in ((FP32, 1, 300, 64), (FP32, 1, 9000, 64), (FP32, 2, 9000, 128), (BF16, 1, 300, 64),
+                           (BF16, 1, 9000, 128), (BF16, 1, 40000, 32)):
+        if N * abs(log_decay) > 80:
+            continue  # the power itself is 0
+        s0 = with_infinities(B, d)
+        q, k, v, _ = tensors(B, N, 2, d, dtype, 4)
+        last = torch.empty_like(s0)
+        vb.linear_attn_fwd(q, k, v, ld, state_in=s0, state_out=last)
+        assert torch.equal(last.isinf(), s0.isinf()) and torch.equal(last[last.isinf()], s0[s0.isinf()]), (dtype, N, d)
+        assert not last.isnan().any()

@@ -22,14 +22,18 @@ __device__ __forceinline__ float lin_pow(float log2_decay, int n) { return exp2f
 // direction each time, is 1e-5 off after a thousand chunks, and 1e-3 after 100000 single tokens.
 struct LinFall {
   float m, base;
+  __device__ __forceinline__ LinFall(float2 v) : m(v.x), base(v.y) {}
   __device__ __forceinline__ LinFall(float log_decay, int n) {
     const float y = log_decay * (float)n;
     const bool slow = fabsf(y) < 0.5f;
     base = slow ? 1.f : 0.f;
     m = slow ? expm1f(y) : lin_pow(lin_log2_decay(log_decay), n);
   }
-  // `s` decayed, plus `a`
-  __device__ __forceinline__ float operator()(float s, float a) const { return fmaf(m, s, a) + (base != 0.f ? s : 0.f); }
+  // `s` decayed, plus `a`; an infinite s stays so (m s is the other infinity, or 0 times it)
+  __device__ __forceinline__ float operator()(float s, float a) const {
+    const float t = fmaf(m, s, a);
+    return base == 0.f ? t : fabsf(s) == INFINITY ? s + a : t + s;
+  }
 };
 
 // The same power as one factor for each of many chunks, rounded so that what one rounding leaves out the next makes up for:

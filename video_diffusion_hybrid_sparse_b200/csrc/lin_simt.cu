@@ -409,9 +409,9 @@ __global__ void __launch_bounds__(128) lin_scan(const __grid_constant__ LinState
     for (int i = 0; i < kAhead; ++i) {
       if (i0 + i >= n) continue;
       const int k = (i0 + i) >> lg, part = (i0 + i) & (sub - 1);
-      const float2 f = part == 0 ? fall[k] : make_float2(1.f, 0.f);
+      const LinFall f(part == 0 ? fall[k] : make_float2(1.f, 0.f));
 #pragma unroll
-      for (int x = 0; x < kE; ++x) s[x] = fmaf(f.x, s[x], a[i][x]) + (f.y != 0.f ? s[x] : 0.f);
+      for (int x = 0; x < kE; ++x) s[x] = f(s[x], a[i][x]);
       if (part == sub - 1) store(wk.s_in + (long long)(j0 + k + 1) * DD + e, s);
     }
   }

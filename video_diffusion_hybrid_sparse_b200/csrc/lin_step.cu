@@ -15,8 +15,8 @@
 // With slots, a CTA looks all of them through for rows that share its own (4 B
 // bytes, from L2, once for each of its tokens): B^2 H D / 32 reads in all, which
 // are nothing for some hundred rows and outweigh the states from about 64 D rows
-// on.  Measured, with slots and without: 700 x 1 x 32 6.1 and 6.3 us, 4096 x 16 x
-// 128 2048 and 1260, 20000 x 1 x 32 234 and 27, 65536 x 1 x 32 3860 and 87.
+// on.  Measured, with slots and without: 700 x 1 x 32 8.5 and 8.9 us, 4096 x 16 x
+// 128 2210 and 1245, 20000 x 1 x 32 236 and 28, 65536 x 1 x 32 3870 and 91.
 #include "lin_common.cuh"
 
 namespace vdn {
