@@ -117,8 +117,8 @@ def build_calls(force: bool = False, verbose: bool = False) -> str:
     libs = cpp_extension.library_paths()
     cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden", "-Wno-attributes",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DVDN_TORCH="{torch.__version__}"',
-           *[f"-I{d}" for d in dirs], src, "-o", CALLS, f"-L{PKG}", "-l:libvdnattn.so", "-Wl,-rpath,$ORIGIN", *[f"-L{d}" for d in libs], "-lc10", "-lc10_cuda",
-           "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+           *[f"-I{d}" for d in dirs], src, "-o", CALLS, f"-L{PKG}", "-l:libvdnattn.so", "-Wl,-rpath,$ORIGIN",
+           *[f"-L{d}" for d in libs], "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)

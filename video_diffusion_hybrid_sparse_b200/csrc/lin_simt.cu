@@ -9,9 +9,10 @@
 // one (271 TFLOP/s of the measured bf16 rate, against 74 of the FMA pipe); it is
 // not written.  The kernel is bound by the FMA pipe, at 2 D (2 D + 64 + 32)
 // operations a row: 64 rows keep the quadratic part at a quarter (D = 128) to a
-// half (64) of it, with the masked blocks of 16 columns and rows behind left out.  To be bound by it, a thread's tile has to
-// turn each load from shared memory into eight operations and more: 8 x 8 of the
-// state and 8 x 4 of the output at D = 128.  fp32 rows come by cp.async, the next
+// half (64) of it, with the masked blocks of 16 columns and rows behind left out.
+// To be bound by it, a thread's tile has to turn each load from shared memory
+// into eight operations and more: 8 x 8 of the state and 8 x 4 of the output at
+// D = 128.  fp32 rows come by cp.async, the next
 // chunk's X while the state is updated.  Measured: 4 x 20000 x 8 x 128 in 1910 us
 // (walk 1560, parts 390), about 40 TFLOP/s executed, 22 of the 4 D^2 operations a
 // row that the formula needs.
