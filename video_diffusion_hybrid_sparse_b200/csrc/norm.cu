@@ -13,7 +13,7 @@
 // pairs: with single operations the e4m3 output is bound by the issue of
 // instructions (118 us for 100 million elements, whatever is read).  Measured:
 // 60480 x 2048 bf16 to e4m3 with groups in 141-158 us (0.84-0.95 of the copy
-// rate), gradients at 46080 x 2048 in 147-149 us (0.78: a row's two sums cross
+// rate), gradients at 46080 x 2048 in 147-150 us (0.78: a row's two sums cross
 // the threads one after the other, which the second does not need: it could go
 // with the first and be multiplied by 1 / rms after).
 #include <cuda_fp8.h>
